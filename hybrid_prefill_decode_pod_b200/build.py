@@ -15,9 +15,11 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libpod_attn.so")
 SOURCES = [os.path.join(CSRC, "pod_kernels.cu"), os.path.join(CSRC, "pod_attn_api.cpp"),
-           os.path.join(CSRC, "pod_static.cu")]
-HEADERS = [os.path.join(CSRC, f) for f in ("pod_plan.h", "pod_ptx.cuh", "pod_exp2.cuh", "pod_prefill.cuh")] + [
-    os.path.join(INCLUDE, "pod_attn.h")]
+           os.path.join(CSRC, "pod_static.cu"), os.path.join(CSRC, "pod_kv4_api.cpp"),
+           os.path.join(CSRC, "pod_kv4_rows.cu"), os.path.join(CSRC, "pod_kv4_decode.cu")]
+HEADERS = [os.path.join(CSRC, f) for f in ("pod_plan.h", "pod_ptx.cuh", "pod_exp2.cuh", "pod_prefill.cuh",
+                                           "pod_device.h", "pod_kv4_params.h", "pod_kv4.cuh")] + [
+    os.path.join(INCLUDE, f) for f in ("pod_attn.h", "pod_kv4.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -49,7 +51,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and not _stale() and not os.environ.get("POD_ATTN_NVCC_EXTRA"):
         return LIB
     tmp = LIB + ".tmp.%d" % os.getpid()
-    cmd = [nvcc(), *NVCC_FLAGS, *extra, "-shared", "-o", tmp, *SOURCES, "-lcudart"]
+    cmd = [nvcc(), *NVCC_FLAGS, *extra, "-t", "0", "-shared", "-o", tmp, *SOURCES, "-lcudart"]
     if verbose:
         print(" ".join(cmd))
     subprocess.check_call(cmd)

@@ -23,6 +23,7 @@
 #include <vector>
 
 #include "pod_attn.h"
+#include "pod_device.h"
 #include "pod_plan.h"
 
 namespace pod {
@@ -49,19 +50,6 @@ constexpr int kDecSplitMax = 1 << 20;
 constexpr int kStatsInts = kMaxSmid * 2;
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = false;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) return;
-    ok = (prev == dev) || (cudaSetDevice(dev) == cudaSuccess);
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-  }
-};
 
 // Capacity layout of the plan buffer: its size bounds any call's plan. A call
 // packs its plan from the start of the buffer (control words, tickets, stats,
@@ -142,8 +130,6 @@ PlanLayout plan_layout(const pod_attn_ctx* c) {
 }
 
 int cuda_fail() { return POD_ECUDA; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int make_map(pod_attn_ctx* c, CUtensorMap* m, const void* base, uint64_t heads, uint64_t rows,
              uint32_t box_rows) {

@@ -1,0 +1,75 @@
+// pod_kv4.cuh -- device helpers of the 4-bit KV cache: row types, the order of
+// the codes inside a record, and the request that a row belongs to.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "pod_kv4_params.h"
+
+namespace pod {
+
+// Two adjacent channels of a bf16 or fp16 row, as fp32 and back (one rounding).
+template <bool FP16>
+__device__ __forceinline__ float2 row2_to_float(uint32_t v) {
+  if constexpr (FP16)
+    return __half22float2(*reinterpret_cast<__half2*>(&v));
+  else
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+
+template <bool FP16>
+__device__ __forceinline__ uint32_t float_to_row2(float a, float b) {
+  if constexpr (FP16) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// Byte offsets inside a record (the orders stated in pod_kv4.h). Eight
+// channels 8 g .. 8 g + 7 of a K token are one word; four channels 4 g ..
+// 4 g + 3 of a V token are one half word.
+template <int D>
+__device__ __forceinline__ int k_code_byte(int token, int g8) {
+  return token * (D / 2) + 4 * ((g8 & 3) * (D / 32) + (g8 >> 2));
+}
+template <int D>
+__device__ __forceinline__ int v_code_byte(int token, int g4) {
+  return 8 * D + 4 * ((32 * (token >> 3) + 4 * (g4 & 7) + ((token & 7) >> 1)) * (D / 32) + (g4 >> 3)) +
+         2 * (token & 1);
+}
+// The pair (s, m) of a token's channel group, K (kv = 0) or V (kv = 1).
+template <int D>
+__device__ __forceinline__ int pair_byte(int kv, int token, int grp, int ngrp) {
+  return kKv4Page * D + ((kv * kKv4Page + token) * ngrp + grp) * 4;
+}
+
+// The request of row i: the largest r with cu[r] <= i, or -1 if cu leaves the
+// row out. cu is read within its num_reqs + 1 entries whatever it holds.
+__device__ __forceinline__ int row_request(const int* __restrict__ cu, int n, int i) {
+  int lo = 0, hi = n;  // cu[lo] <= i < cu[hi] if the row belongs to any
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(cu + mid) <= i)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return __ldg(cu + lo) <= i && i < __ldg(cu + lo + 1) ? lo : -1;
+}
+
+// The record of (request r, position pos, KV head h), or nullptr where the
+// position is outside the table row or the page outside the pool.
+__device__ __forceinline__ unsigned char* record_of(const Kv4Rows& P, int r, long long pos, int h,
+                                                    int rec_bytes) {
+  if (pos < 0 || (pos >> 4) >= P.table_stride) return nullptr;
+  const int page = __ldg(P.table + (long long)r * P.table_stride + (pos >> 4));
+  if (page < 0 || page >= P.pool_blocks) return nullptr;
+  return P.pool + ((long long)page * P.Hk + h) * rec_bytes;
+}
+
+}  // namespace pod

@@ -22,6 +22,7 @@
 #include <mutex>
 
 #include "pod_attn.h"
+#include "pod_device.h"
 #include "pod_plan.h"
 
 namespace pod {
@@ -72,8 +73,6 @@ struct DeviceState {
 constexpr int kMaxDevices = 64;
 DeviceState g_state[kMaxDevices];
 std::mutex g_mu;
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Once per device, with that device current: resolve the array's device
 // address (the host-side symbol is only a stand-in) and set the kernels'

@@ -1,0 +1,495 @@
+"""The 4-bit KV cache on the GPU against its formulas in 64 bits."""
+import math
+
+import pytest
+import torch
+
+import kv4_ref as ref
+from hybrid_prefill_decode_pod_b200 import pod_attn as pa
+from hybrid_prefill_decode_pod_b200 import pod_kv4 as p4
+
+pytestmark = pytest.mark.gpu
+
+BF, HF = torch.bfloat16, torch.float16
+GROUPS = [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128)]
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def table_for(pages, blocks, g):
+    """A block table with the pages of each request anywhere in the pool; the rest is -1."""
+    ids = torch.randperm(blocks, generator=g)[:sum(pages)].to(torch.int32)
+    t = torch.full((len(pages), max(pages + [1])), -1, dtype=torch.int32)
+    at = 0
+    for r, n in enumerate(pages):
+        t[r, :n] = ids[at:at + n]
+        at += n
+    return t
+
+
+def random_pool(blocks, Hk, d, group, g, wild=False):
+    """Records of random codes and pairs; `wild`: pairs of any bits, NaN and infinities too."""
+    rec = p4.record_bytes(d, group)
+    pool = torch.randint(0, 256, (blocks, Hk, rec), generator=g, dtype=torch.uint8)
+    if not wild:
+        n = (rec - 16 * d) // 4
+        s = 0.05 + 0.3 * torch.rand(blocks, Hk, n, generator=g)
+        m = -s * (7.5 + torch.randn(blocks, Hk, n, generator=g))
+        pool[..., 16 * d:] = torch.stack([s, m], -1).half().flatten(-2).contiguous().view(torch.uint8)
+    return pool
+
+
+def rows_case(lens, starts, blocks, seed):
+    g = gen(seed)
+    pages = [-(-(s + n) // 16) for s, n in zip(starts, lens)]
+    table = table_for(pages, blocks, g)
+    cu = torch.tensor([sum(lens[:i]) for i in range(len(lens) + 1)], dtype=torch.int32)
+    return table, cu, torch.tensor(starts, dtype=torch.int32)
+
+
+def row_places(lens, starts, table):
+    """(page id, offset) of each row."""
+    out = []
+    for r, (n, s) in enumerate(zip(lens, starts)):
+        out += [(int(table[r, p // 16]), p % 16) for p in range(s, s + n)]
+    return out
+
+
+LENS = [([1], [0]), ([1, 1, 1, 1, 1], [15, 16, 0, 31, 77]), ([16, 32], [0, 16]),
+        ([0, 5, 0, 40, 17, 0], [3, 14, 0, 8, 1, 0]), ([100, 1, 16], [7, 1000, 9])]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("d,group", GROUPS)
+@pytest.mark.parametrize("lens,starts", LENS)
+def test_write_places_the_codes_and_leaves_the_rest(lens, starts, d, group, dtype):
+    Hk = 3
+    table, cu, start = rows_case(lens, starts, 90, 1)
+    rows = sum(lens)
+    g = gen(2)
+    qkv = (torch.randn(rows + 3, 2 * Hk, d, generator=g) * torch.rand(rows + 3, 2 * Hk, 1, generator=g) * 4).to(dtype)
+    before = random_pool(90, Hk, d, group, g, wild=True)
+    pool, x = before.cuda(), qkv.cuda()
+    kv = p4.PodKv4(Hk, Hk, d, group_size=group, dtype=dtype)
+    # three rows behind the last request
+    kv.write(kv.rows_args(cu.cuda(), start.cuda(), x[:, :Hk], x[:, Hk:], pool, table.cuda()))
+    after = pool.cpu()
+    n, s, m, border = ref.quantised(qkv[:rows].unflatten(1, (2, Hk)), group)   # rows, 2, Hk, d
+    gn, gs, gm = ref.unpack(after, d, group)                                   # blocks, Hk, 2, PAGE, d
+    at = row_places(lens, starts, table)
+    page, off = torch.tensor([a[0] for a in at]), torch.tensor([a[1] for a in at])
+    pick = lambda y: y[page, :, :, off].transpose(1, 2)                        # noqa: E731
+    assert torch.equal(pick(gs), s) and torch.equal(pick(gm), m)
+    far = (pick(gn) - n).abs()
+    assert far[border > 1e-5].max() == 0 and far.max() <= 1
+    # every other token as it was
+    written = torch.zeros(90, 16, dtype=torch.bool)
+    written[page, off] = True
+    code, pair = ref.places(d, group)
+    same = (before == after).all(1)
+    keep = torch.zeros(90, before.shape[-1], dtype=torch.bool)
+    for t in range(16):
+        bytes_t = torch.cat([(code[:, t] // 2).flatten(), 16 * d + 4 * pair[:, t].flatten(), 16 * d + 4 * pair[:, t].flatten() + 1,
+                             16 * d + 4 * pair[:, t].flatten() + 2, 16 * d + 4 * pair[:, t].flatten() + 3]).unique()
+        keep[:, bytes_t] = ~written[:, t:t + 1]
+    assert same[keep].all()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_write_special_values(dtype):
+    """Constant groups, subnormals, values beyond fp16, infinities and NaN."""
+    d, group = 64, 32
+    x = torch.randn(8, 1, d, generator=gen(3))
+    x[0] = 0
+    x[1] = 3.5
+    x[2] *= 1e-7
+    x[3] *= 20000
+    x[4, 0, 5] = math.inf
+    x[5, 0, 40] = math.nan
+    x[6, 0, 0] = -math.inf
+    x[7] = 1.0
+    x[7, 0, 3] = 1.0 + 2.0 ** -7
+    x = x.to(dtype)
+    if dtype == BF:
+        x[3, 0, 1] = 1e38
+    kv = p4.PodKv4(1, 1, d, group_size=group, dtype=dtype)
+    pool = kv.new_pool(1)
+    cu, start = torch.tensor([0, 8], dtype=torch.int32).cuda(), torch.tensor([0], dtype=torch.int32).cuda()
+    tab = torch.zeros(1, 1, dtype=torch.int32).cuda()
+    xc = x.cuda()
+    kv.write(kv.rows_args(cu, start, xc, xc, pool, tab))
+    n, s, m, border = ref.quantised(x, group)
+    gn, gs, gm = (y[0, 0, :, :8] for y in ref.unpack(pool.cpu(), d, group))
+    for kvi in range(2):
+        assert torch.equal(gs[kvi].nan_to_num(-1), s[:, 0].nan_to_num(-1))
+        assert torch.equal(gm[kvi].nan_to_num(-1), m[:, 0].nan_to_num(-1))
+        far = (gn[kvi] - n[:, 0]).abs()
+        far[s[:, 0].isnan()] = 0
+        assert far[border[:, 0] > 1e-5].max() == 0 and far.max() <= 1
+    k, v = torch.zeros_like(xc), torch.zeros_like(xc)
+    kv.read(kv.rows_args(cu, start, k, v, pool, tab))
+    assert torch.equal(k.isnan().cpu(), s.isnan()) and torch.equal(k.nan_to_num(9), v.nan_to_num(9))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("d,group", GROUPS)
+@pytest.mark.parametrize("lens,starts", LENS)
+def test_read_gives_the_rounded_values(lens, starts, d, group, dtype):
+    Hk = 3
+    table, cu, start = rows_case(lens, starts, 90, 4)
+    rows = sum(lens)
+    pool = random_pool(90, Hk, d, group, gen(5))
+    kv = p4.PodKv4(Hk, Hk, d, group_size=group, dtype=dtype)
+    out = torch.full((rows + 2, 2 * Hk, d), 7.0, dtype=dtype).cuda()
+    kv.read(kv.rows_args(cu.cuda(), start.cuda(), out[:, :Hk], out[:, Hk:], pool.cuda(), table.cuda()))
+    val = ref.values(pool, d, group)
+    at = row_places(lens, starts, table)
+    page, off = torch.tensor([a[0] for a in at]), torch.tensor([a[1] for a in at])
+    want = val[page, :, :, off].transpose(1, 2).flatten(1, 2).float().to(dtype)
+    got = out.cpu()
+    assert torch.equal(got[:rows], want)
+    assert (got[rows:] == 7).all()
+
+
+def test_rows_without_a_place():
+    """Positions outside the table and pages outside the pool: not written, read as NaN."""
+    d, group, Hk = 128, 64, 2
+    kv = p4.PodKv4(Hk, Hk, d, group_size=group)
+    table = torch.tensor([[1, -1], [4, 2], [3, 0], [0, 3]], dtype=torch.int32).cuda()   # 4 is outside
+    start = torch.tensor([0, 8, 30, -3], dtype=torch.int32).cuda()
+    cu = torch.tensor([0, 20, 36, 40, 45], dtype=torch.int32).cuda()
+    x = torch.randn(45, Hk, d, generator=gen(6)).to(BF).cuda()
+    pool = kv.new_pool(4)
+    kv.write(kv.rows_args(cu, start, x, x, pool, table))
+    k, v = torch.zeros_like(x), torch.zeros_like(x)
+    kv.read(kv.rows_args(cu, start, k, v, pool, table))
+    bad = torch.zeros(45, dtype=torch.bool)
+    bad[16:20] = True           # page -1
+    bad[20:28] = True           # page 4
+    bad[38:40] = True           # positions 32, 33 of a row of two pages
+    bad[40:43] = True           # positions -3 .. -1
+    for y in (k, v):
+        assert torch.equal(y.isnan().all(-1).all(-1).cpu(), bad) and torch.equal(y.isnan().any(-1).any(-1).cpu(), bad)
+    assert (k[~bad.cuda()].float() - x[~bad.cuda()].float()).abs().max() < 0.5
+
+
+def check_decode(q, pool, table, lens, d, group, o, lse):
+    want, wlse, parts = ref.attend(q.cpu(), pool.cpu(), table.cpu(), lens, d, group)
+    bo, bl = ref.attend_bounds(want, wlse, parts, q.dtype)
+    o, lse = o.cpu().double(), lse.cpu().double()
+    empty = torch.tensor(lens) == 0
+    assert (o[empty] == 0).all() and (lse[empty] == -math.inf).all()
+    assert ((o - want).abs() <= bo)[~empty].all(), ((o - want).abs() / bo).max()
+    assert ((lse - wlse).abs() <= bl)[~empty].all(), ((lse - wlse).abs() / bl)[~empty].max()
+
+
+def run_decode(kv, q, pool, table, lens, stream=None):
+    o = torch.full_like(q, math.nan)
+    lse = torch.full(q.shape[:2], math.nan, device=q.device)
+    kv.decode(kv.decode_args(lens, q, o, lse, pool, table), stream)
+    return o, lse
+
+
+def decode_case(lens, H, Hk, d, group, dtype, seed, blocks=None):
+    g = gen(seed)
+    pages = [-(-n // 16) for n in lens]
+    blocks = blocks or sum(pages) + 3
+    pool = random_pool(blocks, Hk, d, group, g)
+    table = table_for(pages, blocks, g)
+    # what lies behind a length is of any bits
+    wild = random_pool(blocks, Hk, d, group, g, wild=True)
+    code, pair = ref.places(d, group)
+    used = torch.zeros(blocks, dtype=torch.bool)
+    for r, n in enumerate(lens):
+        used[table[r, :pages[r]].long()] = True
+        if n % 16:
+            page = int(table[r, n // 16])
+            for t in range(n % 16, 16):
+                at = torch.cat([(code[:, t] // 2).flatten()] + [16 * d + 4 * pair[:, t].flatten() + b for b in range(4)])
+                pool[page][:, at] = wild[page][:, at]
+    pool[~used] = wild[~used]
+    q = (torch.randn(len(lens), H, d, generator=g) * 1.5).to(dtype)
+    return q, pool, table
+
+
+DECODE = [
+    # lens, H, Hk
+    ([1], 1, 1), ([16], 8, 1), ([17, 1, 0, 15], 4, 2), ([40, 77, 128, 200], 4, 2),
+    ([0, 0], 2, 2), ([3000], 8, 1), ([513, 64, 2048, 31, 33, 1000], 6, 2), ([700] * 9, 15, 3), ([5000, 1, 4096], 14, 2),
+    (list(range(0, 130)), 8, 8),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("d,group", GROUPS)
+@pytest.mark.parametrize("lens,H,Hk", DECODE)
+def test_decode_matches_the_formula(lens, H, Hk, d, group, dtype):
+    q, pool, table = decode_case(lens, H, Hk, d, group, dtype, 7)
+    kv = p4.PodKv4(H, Hk, d, group_size=group, dtype=dtype)
+    qc, pc, tc = q.cuda(), pool.cuda(), table.cuda()
+    lc = torch.tensor(lens, dtype=torch.int32).cuda()
+    o, lse = run_decode(kv, qc, pc, tc, lc)
+    check_decode(q, pool, table, lens, d, group, o, lse)
+    again = run_decode(kv, qc, pc, tc, lc)   # the order of the parts does not change a bit
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
+def test_decode_extreme_queries():
+    """A query of zeros, ones of very large and very small values, and a NaN: each row by itself."""
+    d, group, H, Hk = 128, 64, 4, 1
+    lens = [100] * 6
+    q, pool, table = decode_case(lens, H, Hk, d, group, BF, 8)
+    q[0] = 0
+    q[1] *= 1e6
+    q[2] *= 1e-20
+    q[3, :, 1:] = 0
+    q[4, :, :7] *= 1e4
+    q[5, 2, 9] = math.nan
+    kv = p4.PodKv4(H, Hk, d, group_size=group)
+    o, lse = run_decode(kv, q.cuda(), pool.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda())
+    assert o[5, 2].isnan().all() and lse[5, 2].isnan()
+    assert not o[5, [0, 1, 3]].isnan().any() and not o[:5].isnan().any()
+    check_decode(q[:5], pool, table[:5], lens[:5], d, group, o[:5], lse[:5])
+
+
+def test_decode_keys_of_nan_and_bad_pages_touch_their_request_only():
+    d, group, H, Hk = 128, 32, 8, 2
+    lens = [300, 300, 5000, 40, 300]
+    q, pool, table = decode_case(lens, H, Hk, d, group, BF, 9)
+    table[1, 7] = pool.shape[0]
+    table[2, 200] = -5
+    pool[int(table[4, 3]), 1, 16 * d:16 * d + 4] = 255   # s, m of one token's first group of K, head 1
+    lc = torch.tensor(lens, dtype=torch.int32).cuda()
+    kv = p4.PodKv4(H, Hk, d, group_size=group)
+    o, lse = run_decode(kv, q.cuda(), pool.cuda(), table.cuda(), lc)
+    assert o[[1, 2]].isnan().all() and lse[[1, 2]].isnan().all()
+    assert o[4, 4:].isnan().all() and lse[4, 4:].isnan().all() and not o[4, :4].isnan().any()
+    ok = [0, 3]
+    check_decode(q[ok], pool, table[ok], [lens[i] for i in ok], d, group, o[ok], lse[ok])
+
+
+def test_decode_lengths_beyond_the_table_are_cut():
+    q, pool, table = decode_case([64, 64], 4, 2, 64, 64, HF, 10)
+    kv = p4.PodKv4(4, 2, 64, group_size=64, dtype=HF)
+    lens = torch.tensor([2 ** 31 - 1, -7], dtype=torch.int32).cuda()
+    o, lse = run_decode(kv, q.cuda(), pool.cuda(), table.cuda(), lens)
+    check_decode(q, pool, table, [64, 0], 64, 64, o, lse)
+
+
+def test_decode_far_pages():
+    """Records whose byte offsets pass 32 bits."""
+    d, group, H, Hk = 128, 64, 4, 4
+    lens = [200, 50]
+    q, small, table = decode_case(lens, H, Hk, d, group, BF, 11)
+    blocks = (1 << 33) // (Hk * small.shape[-1])
+    kv = p4.PodKv4(H, Hk, d, group_size=group)
+    pool = torch.empty(blocks, Hk, small.shape[-1], dtype=torch.uint8, device="cuda")
+    far = blocks - small.shape[0]
+    pool[far:] = small.cuda()
+    tc = (table + far * (table >= 0)).int().cuda()
+    lc = torch.tensor(lens, dtype=torch.int32).cuda()
+    o, lse = run_decode(kv, q.cuda(), pool, tc, lc)
+    check_decode(q, small, table, lens, d, group, o, lse)
+    cu = torch.tensor([0, 200, 250], dtype=torch.int32).cuda()
+    start = torch.zeros(2, dtype=torch.int32).cuda()
+    k, v = (torch.zeros(250, Hk, d, dtype=BF, device="cuda") for _ in range(2))
+    kv.read(kv.rows_args(cu, start, k, v, pool, tc))
+    k2, v2 = torch.zeros_like(k), torch.zeros_like(v)
+    kv.read(kv.rows_args(cu, start, k2, v2, small.cuda(), table.cuda()))
+    assert torch.equal(k, k2) and torch.equal(v, v2)
+    kv.write(kv.rows_args(cu, start, k, v, pool, tc))
+    kv.read(kv.rows_args(cu, start, k2, v2, pool, tc))
+    # a value written again moves by half a step of its group at most (the rows are rounded), a step here
+    assert (k2.float() - k.float()).abs().max() < 0.4
+
+
+ROPE = [(1, 32, 8, 128, 128), (7, 4, 2, 64, 64), (33, 3, 1, 128, 64), (5, 2, 3, 64, 48), (65, 8, 8, 128, 16), (3, 5, 0, 128, 112), (300, 64, 8, 128, 128)]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("norm", ["both", "none", "q"])
+@pytest.mark.parametrize("rows,H,Hk,d,rot", ROPE)
+def test_norm_rope(rows, H, Hk, d, rot, norm, interleaved, dtype):
+    g = gen(12)
+    qkv = (torch.randn(rows, H + 2 * Hk + 1, d, generator=g) * 3).to(dtype)
+    qkv[0, 0] = 0
+    w = [(1 + 0.3 * torch.randn(d, generator=g)).to(dtype) if norm == "both" or (norm == "q" and i == 0) else None for i in range(2)]
+    table = p4.rope_table(9000, rot, 10000.0, device="cpu")
+    pos = torch.randint(0, 9000, (rows,), generator=g, dtype=torch.int32)
+    pos[-1] = 8999
+    x = qkv.cuda()
+    q, k = x[:, :H], x[:, H:H + Hk] if Hk else None
+    wc = [y.cuda() if y is not None else None for y in w]
+    qo = torch.empty(rows, H, d, dtype=dtype, device="cuda")
+    ko = torch.empty(Hk, rows, d, dtype=dtype, device="cuda").transpose(0, 1) if Hk else None
+    kw = dict(q_weight=wc[0], k_weight=wc[1] if Hk else None, eps=1e-5, interleaved=interleaved)
+    p4.qk_norm_rope(p4.norm_rope_args(q, k, pos.cuda(), table.cuda(), q_out=qo, k_out=ko, **kw))
+    for got, src, wt in ((qo, qkv[:, :H], w[0]), (ko, qkv[:, H:H + Hk], w[1])):
+        if got is None:
+            continue
+        want, size = ref.norm_rope(src, wt, table, pos, 1e-5, interleaved)
+        # half a step of the output; 13 fp32 roundings of 2^-24 on the way (squares and their sum
+        # count half); fp16 below 2^-14 is spaced by 2^-24
+        bound = ref.EPS[dtype] / 2 * want.abs() + 2.0 ** -20 * size + 2.0 ** -25
+        assert ((got.cpu().double() - want).abs() <= bound).all()
+    # in place
+    p4.qk_norm_rope(p4.norm_rope_args(q, k, pos.cuda(), table.cuda(), **kw))
+    assert torch.equal(q, qo) and (k is None or torch.equal(k, ko))
+    assert torch.equal(x[:, H + Hk:].cpu(), qkv[:, H + Hk:])
+
+
+def test_norm_rope_padding_and_far_positions():
+    x = torch.randn(4, 3, 64, generator=gen(13)).to(BF).cuda()
+    before = x.clone()
+    pos = torch.tensor([3, -1, 100, 99], dtype=torch.int32).cuda()
+    p4.qk_norm_rope(p4.norm_rope_args(x[:, :2], x[:, 2:], pos, p4.rope_table(100, 32)))
+    assert torch.equal(x[1], before[1])
+    assert x[2].isnan().all() and not x[[0, 3]].isnan().any()
+
+
+def step(kv, x, pool, table, lens, cu, tab, w, bufs):
+    """One decode step of a layer: norm and rotate the new token, write it, attend."""
+    H, Hk = kv.cfg.num_qo_heads, kv.cfg.num_kv_heads
+    q, k, o, lse = bufs
+    p4.qk_norm_rope(p4.norm_rope_args(x[:, :H], x[:, H:H + Hk], lens, tab, q_out=q, k_out=k, q_weight=w, k_weight=w))
+    kv.write(kv.rows_args(cu, lens, k, x[:, H + Hk:], pool, table))
+    kv.decode(kv.decode_args(lens + 1, q, o, lse, pool, table))
+
+
+def test_decode_steps_captured_and_replayed():
+    """A chain of all operators, captured once; replays with other tokens and lengths give what eager calls give."""
+    H, Hk, d, R = 8, 2, 128, 5
+    kv, g = p4.PodKv4(H, Hk, d, group_size=64), gen(14)
+    tab = p4.rope_table(512, d)
+    w = (1 + 0.1 * torch.randn(d, generator=g)).to(BF).cuda()
+    table = torch.randperm(R * 8, generator=g).reshape(R, 8).to(torch.int32).cuda()
+    cu = torch.arange(R + 1, dtype=torch.int32).cuda()
+    pools = [kv.new_pool(R * 8) for _ in range(2)]
+    lens = torch.tensor([0, 3, 15, 16, 100], dtype=torch.int32).cuda()
+    bufs = [tuple(torch.zeros(R, n, d, dtype=BF, device="cuda") for n in (H, Hk, H)) + (torch.zeros(R, H, device="cuda"),) for _ in range(2)]
+    x = torch.zeros(R, H + 2 * Hk, d, dtype=BF, device="cuda")
+    step(kv, x, pools[0].clone(), table, lens, cu, tab, w, bufs[0])   # warm up
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step(kv, x, pools[0], table, lens, cu, tab, w, bufs[0])
+        lens += 1
+    other = torch.tensor([0, 3, 15, 16, 100], dtype=torch.int32).cuda()
+    history = []
+    for i in range(6):
+        x.copy_(torch.randn(x.shape, generator=g).to(BF))
+        graph.replay()
+        step(kv, x, pools[1], table, other, cu, tab, w, bufs[1])
+        other += 1
+        torch.cuda.synchronize()
+        assert torch.equal(lens, other) and torch.equal(pools[0], pools[1])
+        assert all(torch.equal(a, b) for a, b in zip(*bufs))
+        history.append(bufs[1][2].clone())
+    assert not torch.equal(history[0], history[1])
+    q = bufs[1][0]
+    check_decode(q.cpu(), pools[1].cpu(), table.cpu(), other.tolist(), d, 64, bufs[1][2], bufs[1][3])
+
+
+def test_other_stream_and_two_contexts():
+    """Calls on a side stream, beside calls of another context on the main one."""
+    lens = [900, 100, 33]
+    q, pool, table = decode_case(lens, 8, 2, 128, 64, BF, 15)
+    kvs = [p4.PodKv4(8, 2, 128) for _ in range(2)]
+    qc, pc, tc, lc = q.cuda(), pool.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for _ in range(20):
+        outs.append(run_decode(kvs[0], qc, pc, tc, lc))
+        with torch.cuda.stream(side):
+            outs.append(run_decode(kvs[1], qc, pc, tc, lc))
+    torch.cuda.synchronize()
+    for o, lse in outs[1:]:
+        assert torch.equal(o, outs[0][0]) and torch.equal(lse, outs[0][1])
+    check_decode(q, pool, table, lens, 128, 64, *outs[0])
+
+
+def test_chunked_prefill_over_the_cache():
+    """Norm and rotate a chunk, write it, read the whole context back and run the bf16 prefill on
+    it beside the 4-bit decodes: attention over the values that the cache holds."""
+    H, Hk, d, group, prior, chunk = 8, 2, 128, 32, 150, 70
+    g = gen(16)
+    kv = p4.PodKv4(H, Hk, d, group_size=group)
+    pod = pa.PodAttention(H, Hk, d, max_prefill_reqs=1, max_prefill_tokens=chunk, max_decode_reqs=1, max_kv_tokens=512)
+    pool = random_pool(40, Hk, d, group, g).cuda()
+    table = torch.randperm(40, generator=g)[:16].reshape(1, 16).to(torch.int32).cuda()
+    tab = p4.rope_table(512, d)
+    x = torch.randn(chunk, H + 2 * Hk, d, generator=g).to(BF).cuda()
+    q = torch.empty(chunk, H, d, dtype=BF, device="cuda")
+    k = torch.empty(chunk, Hk, d, dtype=BF, device="cuda")
+    pos = torch.arange(prior, prior + chunk, dtype=torch.int32, device="cuda")
+    p4.qk_norm_rope(p4.norm_rope_args(x[:, :H], x[:, H:H + Hk], pos, tab, q_out=q, k_out=k))
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
+    kv.write(kv.rows_args(i32(0, chunk), i32(prior), k, x[:, H + Hk:], pool, table))
+    n = prior + chunk
+    kc, vc = (torch.empty(n, Hk, d, dtype=BF, device="cuda") for _ in range(2))
+    kv.read(kv.rows_args(i32(0, n), i32(0), kc, vc, pool, table))
+    o = torch.empty_like(q)
+    lse = torch.empty(chunk, H, device="cuda")
+    pod.prefill_only(pod.prefill_args([chunk], [prior], q, o, lse, k=[kc], v=[vc]))
+    assert pod.status() == pa.POD_OK and pod.close() == pa.POD_OK
+    # the last token's row is what a decode over the cache gives
+    do, dl = run_decode(kv, q[-1:].contiguous(), pool, table, i32(n))
+    check_decode(q[-1:].cpu(), pool.cpu(), table.cpu(), [n], d, group, do, dl)
+    val = ref.values(pool.cpu()[table.cpu()[0].long()], d, group).permute(2, 1, 0, 3, 4).flatten(2, 3)
+    for t in (0, 5, chunk - 1):
+        for h in (0, 7):
+            kk, vv = val[0, h // 4, :prior + t + 1], val[1, h // 4, :prior + t + 1]
+            sc = kk @ q[t, h].cpu().double() / math.sqrt(d)
+            want = torch.softmax(sc, 0) @ vv
+            # the prefill's tolerances, and the rounding of the rows that were read back (2^-8 of
+            # a key moves a score by at most 2^-8 sum |q_i k_i| / sqrt(d))
+            size = (kk.abs() @ q[t, h].cpu().double().abs()).max() / math.sqrt(d) * 2.0 ** -8
+            assert (o[t, h].cpu().double() - want).abs().max() <= 1e-2 + (2 * size + 2.0 ** -8) * vv.abs().max()
+            assert abs(lse[t, h].item() - torch.logsumexp(sc, 0).item()) <= 1e-3 + size
+
+
+def test_calls_with_nothing_to_do():
+    kv = p4.PodKv4(4, 2, 64)
+    pool = kv.new_pool(1)
+    e = lambda *s, t=BF: torch.empty(*s, dtype=t, device="cuda")  # noqa: E731
+    i32 = torch.int32
+    kv.write(kv.rows_args(torch.zeros(1, dtype=i32).cuda(), e(0, t=i32), e(0, 2, 64), e(0, 2, 64), pool, e(0, 3, t=i32)))
+    kv.read(kv.rows_args(torch.zeros(3, dtype=i32).cuda(), torch.zeros(2, dtype=i32).cuda(), e(0, 2, 64), e(0, 2, 64), pool, e(2, 3, t=i32)))
+    kv.decode(kv.decode_args(e(0, t=i32), e(0, 4, 64), e(0, 4, 64), e(0, 4, t=torch.float32), pool, e(0, 3, t=i32)))
+    p4.qk_norm_rope(p4.norm_rope_args(e(0, 4, 64), e(0, 2, 64), e(0, t=i32), p4.rope_table(4, 64)))
+    # rows of no request
+    x = torch.full((3, 2, 64), 5.0, dtype=BF, device="cuda")
+    kv.read(kv.rows_args(torch.zeros(2, dtype=i32).cuda(), torch.zeros(1, dtype=i32).cuda(), x, x.clone(), pool, torch.zeros(1, 1, dtype=i32).cuda()))
+    assert (x == 5).all()
+    o, lse = run_decode(kv, e(2, 4, 64).zero_(), pool, e(2, 0, t=i32), torch.tensor([5, 0], dtype=i32).cuda())
+    assert (o == 0).all() and (lse == -math.inf).all()
+
+
+def test_context_errors():
+    for kw, code in ((dict(device=99), pa.POD_EINVAL), (dict(group_size=48), pa.POD_EUNSUPPORTED)):
+        with pytest.raises(pa.PodError) as e:
+            p4.PodKv4(4, 2, 64, **kw)
+        assert e.value.code == code
+    kv = p4.PodKv4(4, 2, 64, max_decode_reqs=2)
+    pool = kv.new_pool(1)
+    q = torch.zeros(3, 4, 64, dtype=BF, device="cuda")
+    lens, tab = torch.zeros(3, dtype=torch.int32).cuda(), torch.zeros(3, 1, dtype=torch.int32).cuda()
+    with pytest.raises(pa.PodError) as e:
+        run_decode(kv, q, pool, tab, lens)
+    assert e.value.code == pa.POD_ECAPACITY
+    with pytest.raises(ValueError):
+        run_decode(kv, q.half(), pool, tab, lens)
+    with pytest.raises(ValueError):
+        run_decode(kv, q, pool, tab.long(), lens)
+    with pytest.raises(ValueError):
+        run_decode(kv, q, pool[:, :, :-1], tab, lens)
+    with pytest.raises(ValueError):
+        kv.rows_args(lens, lens, q, q, pool, tab)
+    assert kv.close() == pa.POD_OK
+    with pytest.raises(ValueError):
+        run_decode(kv, q[:2], pool, tab[:2], lens[:2])
