@@ -18,7 +18,7 @@ SOURCES = [os.path.join(CSRC, "pod_kernels.cu"), os.path.join(CSRC, "pod_attn_ap
            os.path.join(CSRC, "pod_static.cu"), os.path.join(CSRC, "pod_kv4_api.cpp"),
            os.path.join(CSRC, "pod_kv4_rows.cu"), os.path.join(CSRC, "pod_kv4_decode.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("pod_plan.h", "pod_ptx.cuh", "pod_exp2.cuh", "pod_prefill.cuh",
-                                           "pod_device.h", "pod_kv4_params.h", "pod_kv4.cuh")] + [
+                                           "pod_device.h", "pod_kv4_params.h", "pod_kv4_split.h", "pod_kv4.cuh")] + [
     os.path.join(INCLUDE, f) for f in ("pod_attn.h", "pod_kv4.h")]
 
 NVCC_FLAGS = [

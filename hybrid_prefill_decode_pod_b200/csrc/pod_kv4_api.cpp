@@ -181,7 +181,7 @@ int pod_kv4_create(pod_kv4_ctx** out, const pod_kv4_config* cfg) {
   if (rc) return rc;
   if (H / Hk > kMaxGroup || cfg->page_size != kKv4Page) return POD_EUNSUPPORTED;
   if (cfg->dtype != POD_DTYPE_BF16 && cfg->dtype != POD_DTYPE_FP16) return POD_EUNSUPPORTED;
-  if (cfg->max_decode_reqs > kKv4MaxReqs || Hk > (1 << 16)) return POD_ECAPACITY;
+  if (cfg->max_decode_reqs > kKv4MaxReqs || Hk > 512) return POD_ECAPACITY;
   rc = check_device(cfg->device);
   if (rc) return rc;
   DeviceGuard guard(cfg->device);
@@ -198,7 +198,8 @@ int pod_kv4_create(pod_kv4_ctx** out, const pod_kv4_config* cfg) {
   c->cfg = *cfg;
   int per_sm = 0;
   size_t floats = 0;
-  if (kv4_decode_init(cfg->head_dim, cfg->group_size, cfg->dtype, H / Hk, &per_sm, &floats) !=
+  if (kv4_decode_init(cfg->head_dim, cfg->group_size, cfg->dtype, H / Hk, cfg->max_decode_reqs,
+                      &per_sm, &floats) !=
           cudaSuccess ||
       per_sm < 1) {
     delete c;

@@ -1,121 +1,663 @@
 // pod_kv4_decode.cu -- single-token GQA attention over the 4-bit KV cache.
+//
+// Bound by the cache's bytes: 16 D + 128 D / group for 16 tokens of one head
+// (2304 at D = 128, groups of 64). At 6.5 TB/s an SM takes one such record in
+// about 100 cycles, so a warp instruction for every 32 pairs of codes costs a
+// sixth of the issue slots and the unpacking decides:
+//
+//  * K K^T q as matrix products with the codes themselves. A code n in the low
+//    bits of an fp16 is the subnormal n 2^-24, exactly: one AND makes two of
+//    them (the codes in bits 4..7 are n 2^-20, undone in the query). The
+//    queries are scaled by a power of two so that their largest channel lies in
+//    [2^9, 2^10); 2^-31 of it is then the rounding of the others. Tokens are
+//    the rows of the product and the G <= 8 heads its columns, so no row is
+//    padding. Each channel group is summed by itself in fp32 and
+//    score = s (sum q n) + m (sum q) joins them.
+//  * V^T p as well: rows are channels, columns heads. Here the weights p s
+//    multiply the codes; they need the exponents of bf16 (in a long context
+//    p s runs below fp16's 2^-14 for tokens that still count together), one
+//    rounding of 2^-8 of each weight, the step of a bf16 output. An AND-OR makes
+//    two bf16 128 + n, and a product with rows of -128 takes the same rounded
+//    weights away again, every 64 tokens, before the sum is long. sum p m is
+//    added in fp32.
+//  * The running maximum and sum, scores, weights and O are fp32; one rescale
+//    every 64 tokens.
+//
+// Work: see pod_kv4_split.h. The line of blocks is cut into equal parts over
+// the CTAs and each of those over its warps, so lengths need no balance and no
+// plan from the host. Warps stream their blocks through rings of their own
+// (cp.async), across segments. What a warp has of a segment that it does not
+// hold whole is joined first in its CTA, then, where the segment leaves the
+// CTA, through the workspace by the CTA that arrives last, in the order of the
+// tokens: the result does not depend on the order of arrival.
 #include "pod_kv4.cuh"
+#include "pod_kv4_split.h"
 
 namespace pod {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTile = 4;   // blocks of 16 tokens between two rescales
+constexpr int kSlots = 8;  // blocks in a warp's ring
 constexpr int kMaxG = 8;
+constexpr int kLeast = 16;  // blocks that make another CTA worth its join
+constexpr float kLn2 = 0.69314718055994531f;
 
-// One CTA for each (request, KV head); each warp takes every eighth token with
-// its own running maximum and sum, which are joined through shared memory.
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// (a & mask) | bits in one instruction
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(mask), "r"(bits));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// N words of shared memory, N = 1, 2 or 4
+template <int N>
+__device__ __forceinline__ void lds(uint32_t (&v)[N], const unsigned char* p) {
+  if constexpr (N == 4) {
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+  } else if constexpr (N == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    v[0] = x.x; v[1] = x.y;
+  } else {
+    v[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+__device__ __forceinline__ float2 pair(uint32_t v) {
+  return __half22float2(*reinterpret_cast<__half2*>(&v));
+}
+
+// max or sum over the eight rows of a fragment (lanes 4 apart)
+__device__ __forceinline__ float rows_max(float x) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+__device__ __forceinline__ float rows_sum(float x) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// What a warp has of the segment at the start or the end of its blocks.
+struct PieceMeta {
+  int has[2];  // [0] goes on from the blocks before, [1] begins here and goes on
+  int ends0;   // [0] reaches the end of its segment
+  int r[2], h[2];
+};
+
+template <int D, int GROUP>
+struct Shape {
+  static constexpr int kRec = kv4_record_bytes(D, GROUP);
+  static constexpr int NG = D / GROUP, NC = D / 32;  // channel groups, chunks of 32 channels
+  static constexpr int kRing = kSlots * kRec;
+  // shared memory: rings, partial results [warp][G][D] and their (max, sum),
+  // pieces, then the requests' first blocks
+  static constexpr int kMlOff = kWarps * kRing;  // float [warp][2][kMaxG][2]
+  static constexpr int kMetaOff = kMlOff + kWarps * 2 * kMaxG * 2 * 4;
+  static constexpr int kMiscOff = kMetaOff + kWarps * (int)sizeof(PieceMeta);
+  static constexpr int kPartOff = (kMiscOff + 64 + 15) / 16 * 16;
+  static __host__ __device__ int part_bytes(int G) { return kWarps * G * D * 4; }
+  static __host__ __device__ int smem(int G, int reqs) {
+    return kPartOff + part_bytes(G) + (reqs + 1) * 4;
+  }
+};
+
 template <int D, int GROUP, bool FP16>
-__global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4Decode P) {
-  constexpr int kCh = D / 32, NG = D / GROUP, kRec = kv4_record_bytes(D, GROUP);
-  __shared__ float so[kWarps][kMaxG][D];
-  __shared__ float sm[kWarps][kMaxG], sl[kWarps][kMaxG];
-  const int r = blockIdx.x, h = blockIdx.y, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long cap = (long long)P.table_stride * kKv4Page;
-  const int len = (int)min((long long)max(P.ctx_lens[r], 0), cap);
-  float q[kMaxG][kCh], o[kMaxG][kCh], mx[kMaxG], l[kMaxG];
+__global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode P) {
+  using S = Shape<D, GROUP>;
+  constexpr int NG = S::NG, NC = S::NC, kRec = S::kRec;
+  extern __shared__ __align__(128) unsigned char smem[];
+  float* ml = reinterpret_cast<float*>(smem + S::kMlOff);
+  PieceMeta* meta = reinterpret_cast<PieceMeta*>(smem + S::kMetaOff);
+  int* misc = reinterpret_cast<int*>(smem + S::kMiscOff);
+  float* part0 = reinterpret_cast<float*>(smem + S::kPartOff);
+  int* first = reinterpret_cast<int*>(smem + S::kPartOff + S::part_bytes(P.G));
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, row = lane >> 2, j = lane & 3;
+  const int R = P.num_reqs, Hk = P.Hk, G = P.G;
+  const long long cap = min((long long)P.table_stride * kKv4Page, (1LL << 31) - 16);
+  const auto length = [&](int r) { return (int)min((long long)max(__ldg(P.ctx_lens + r), 0), cap); };
+
+  // first[r]: blocks of one head in front of request r
+  {
+    const int each = (R + kThreads - 1) / kThreads, r0 = min(tid * each, R), r1 = min(r0 + each, R);
+    int sum = 0;
+    for (int r = r0; r < r1; ++r) sum += (length(r) + 15) >> 4;
+    int inc = sum;
 #pragma unroll
-  for (int g = 0; g < kMaxG; ++g) {
-    mx[g] = -INFINITY;
-    l[g] = 0.f;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) misc[w] = inc;
+    if (tid < kWarps) meta[tid].has[0] = meta[tid].has[1] = 0;
+    __syncthreads();
+    int before = inc - sum;
+    for (int x = 0; x < w; ++x) before += misc[x];
+    for (int r = r0; r < r1; ++r) {
+      first[r] = before;
+      before += (length(r) + 15) >> 4;
+    }
+    if (tid == kThreads - 1) first[R] = before;
+    __syncthreads();
+  }
+  const long long W = (long long)first[R] * Hk;
+
+  // empty contexts
+  for (int r = blockIdx.x; r < R; r += gridDim.x) {
+    if (first[r] != first[r + 1]) continue;
+    uint32_t* o = reinterpret_cast<uint32_t*>(P.o + (long long)r * P.H * D);
+    for (int i = tid; i < P.H * D / 2; i += kThreads) o[i] = 0;
+    for (int i = tid; i < P.H; i += kThreads) P.lse[(long long)r * P.H + i] = -INFINITY;
+  }
+  if (W == 0) return;
+  const int N = kv4_workers(W, gridDim.x, kLeast), cta = blockIdx.x;
+  if (cta >= N) return;
+
+  // ------------------------------------------------ this warp's blocks
+  const long long cb = kv4_begin(W, N, cta), ce = kv4_begin(W, N, cta + 1);
+  const long long xb = cb + kv4_begin(ce - cb, kWarps, w), xe = cb + kv4_begin(ce - cb, kWarps, w + 1);
+  const int total = (int)(xe - xb);
+  unsigned char* ring = smem + w * S::kRing;
+  const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring) + lane * 16;
+
+  // Lane i of `cur` has the record of block 32 b + i, of `nxt` that of the 32
+  // behind; -1 where the page id lies outside the pool.
+  bool any_bad = false;
+  const auto records = [&](int base) {
+    int rec = 0;
+    if (base + lane < total) {
+      const Kv4Place p = kv4_place(first, R, Hk, xb + base + lane);
+      const int page = __ldg(P.table + (long long)p.r * P.table_stride + p.blk);
+      rec = page >= 0 && page < P.pool_blocks ? page * Hk + p.h : -1;
+    }
+    return rec;
+  };
+  int cur = records(0), nxt = records(32);
+  int issued = 0, islot = 0;
+  const auto issue = [&]() {
+    if (issued < total) {
+      if ((issued & 31) == 0 && issued) {
+        cur = nxt;
+        nxt = records(issued + 32);
+      }
+      const int rec = __shfl_sync(0xffffffffu, cur, issued & 31);
+      if (rec >= 0) {
+        const unsigned char* src = P.pool + (long long)rec * kRec + lane * 16;
+        const uint32_t dst = ring_s + islot * kRec;
 #pragma unroll
-    for (int c = 0; c < kCh; ++c) {
-      o[g][c] = 0.f;
-      const int ch = 32 * c + lane;
-      q[g][c] = 0.f;
-      if (g < P.G) {
-        const float2 f = row2_to_float<FP16>(
-            P.q[((long long)r * P.H + h * P.G + g) * D + ch]);
-        q[g][c] = f.x;
+        for (int i = 0; i < kRec / 512; ++i) cp16(dst + i * 512, src + i * 512);
+        if (kRec % 512 && lane < kRec % 512 / 16)
+          cp16(dst + kRec / 512 * 512, src + kRec / 512 * 512);
+      } else {
+        any_bad = true;
       }
     }
-  }
-  for (int t = w; t < len; t += kWarps) {
-    const int page = __ldg(P.table + (long long)r * P.table_stride + (t >> 4)), tt = t & 15;
-    const bool good = page >= 0 && page < P.pool_blocks;
-    const unsigned char* rec = P.pool + ((long long)(good ? page : 0) * P.Hk + h) * kRec;
-    float k[kCh], v[kCh];
+    ++issued;
+    islot = islot + 1 == kSlots ? 0 : islot + 1;
+    cp_commit();
+  };
+  for (int i = 0; i < kSlots; ++i) issue();
+
+  int slot = 0;
+  for (long long x = xb; x < xe;) {
+    const Kv4Place seg = kv4_place(first, R, Hk, x);
+    const int n = (int)min((long long)(seg.nblk - seg.blk), xe - x);
+    const int len = length(seg.r);
+    const long long orow = (long long)seg.r * P.H + (long long)seg.h * G;
+
+    // The queries as the second operand: column `row` is a head, chunk c's
+    // channels 32 c + 8 j + i in the order in which K's codes come apart.
+    uint32_t qf[NC][4];
+    float qs[NG][2], F[2];
+    {
+      float q[NC][8], big = 0.f;
 #pragma unroll
-    for (int c = 0; c < kCh; ++c) {
-      const int ch = 32 * c + lane;
-      const int kb = rec[k_code_byte<D>(tt, ch >> 3) + ((ch & 7) >> 1)] >> (4 * (ch & 1)) & 15;
-      const int vb = rec[v_code_byte<D>(tt, ch >> 2) + ((ch & 3) >> 1)] >> (4 * (ch & 1)) & 15;
-      const __half2 kp = *reinterpret_cast<const __half2*>(rec + pair_byte<D>(0, tt, ch / GROUP, NG));
-      const __half2 vp = *reinterpret_cast<const __half2*>(rec + pair_byte<D>(1, tt, ch / GROUP, NG));
-      k[c] = fmaf((float)kb, __low2float(kp), __high2float(kp));
-      v[c] = fmaf((float)vb, __low2float(vp), __high2float(vp));
-      if (!good) k[c] = v[c] = __int_as_float(0x7fffffff);
+      for (int c = 0; c < NC; ++c) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row < G)
+          v = __ldg(reinterpret_cast<const uint4*>(P.q + (orow + row) * D + 32 * c + 8 * j));
+        const uint32_t vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = row2_to_float<FP16>(vv[i]);
+          q[c][2 * i] = f.x;
+          q[c][2 * i + 1] = f.y;
+          big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+          if (!(fabsf(f.x) < INFINITY && fabsf(f.y) < INFINITY)) big = INFINITY;
+        }
+      }
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      const int e = __float_as_int(big) >> 23;
+      const float sc = e == 0 || e == 255 ? 1.f : __int_as_float(min(263 - e, 254) << 23);
+      const float f = P.scale_log2 * 16777216.f / sc;
+      float sum[NG];
+#pragma unroll
+      for (int g = 0; g < NG; ++g) sum[g] = 0.f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          q[c][i] *= sc;
+          sum[c * 32 / GROUP] += q[c][i];
+        }
+        qf[c][0] = float_to_row2<true>(q[c][0], q[c][4]);
+        qf[c][1] = float_to_row2<true>(q[c][1] * 0.0625f, q[c][5] * 0.0625f);
+        qf[c][2] = float_to_row2<true>(q[c][2], q[c][6]);
+        qf[c][3] = float_to_row2<true>(q[c][3] * 0.0625f, q[c][7] * 0.0625f);
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+        qs[g][0] = __shfl_sync(0xffffffffu, sum[g], 8 * j) * 0x1p-24f;
+        qs[g][1] = __shfl_sync(0xffffffffu, sum[g], 8 * j + 4) * 0x1p-24f;
+      }
+      F[0] = __shfl_sync(0xffffffffu, f, 8 * j);
+      F[1] = __shfl_sync(0xffffffffu, f, 8 * j + 4);
+    }
+
+    // State of heads 2 j and 2 j + 1: O of channels 32 c + 4 row + 0..3 (tile t,
+    // rows `row` and `row` + 8 are channels 2 t and 2 t + 1), this lane's part
+    // of the sums of p and of p m.
+    float O[NC][2][4], pm[NG][2], l[2] = {0.f, 0.f}, top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) O[c][t][i] = 0.f;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) pm[g][0] = pm[g][1] = 0.f;
+
+    for (int t0 = 0; t0 < n; t0 += kTile) {
+      const int nb = min(kTile, n - t0);
+      cp_wait<kSlots - kTile>();
+      __syncwarp();
+      // ---- scores of the tile's tokens: rows `row`, `row` + 8 of each block
+      float p[kTile][4];
+#pragma unroll
+      for (int b = 0; b < kTile; ++b) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[b][i] = -INFINITY;
+        if (b < nb) {
+          const int sl = slot + b >= kSlots ? slot + b - kSlots : slot + b;
+          const unsigned char* rec = ring + sl * kRec;
+          uint32_t ka[NC], kb[NC], pa[NG], pb[NG];
+          lds<NC>(ka, rec + lane * (D / 8));
+          lds<NC>(kb, rec + 4 * D + lane * (D / 8));
+          lds<NG>(pa, rec + 16 * D + row * NG * 4);
+          lds<NG>(pb, rec + 16 * D + (row + 8) * NG * 4);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[b][i] = 0.f;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = g * GROUP / 32; c < (g + 1) * GROUP / 32; ++c) {
+              mma_f16(acc, ka[c] & 0x000f000fu, kb[c] & 0x000f000fu, ka[c] & 0x00f000f0u,
+                      kb[c] & 0x00f000f0u, qf[c][0], qf[c][1]);
+              const uint32_t a8 = ka[c] >> 8, b8 = kb[c] >> 8;
+              mma_f16(acc, a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u,
+                      b8 & 0x00f000f0u, qf[c][2], qf[c][3]);
+            }
+            const float2 sa = pair(pa[g]), sb = pair(pb[g]);
+            p[b][0] = fmaf(sa.x, acc[0], fmaf(sa.y, qs[g][0], p[b][0]));
+            p[b][1] = fmaf(sa.x, acc[1], fmaf(sa.y, qs[g][1], p[b][1]));
+            p[b][2] = fmaf(sb.x, acc[2], fmaf(sb.y, qs[g][0], p[b][2]));
+            p[b][3] = fmaf(sb.x, acc[3], fmaf(sb.y, qs[g][1], p[b][3]));
+          }
+        }
+      }
+      // tokens behind the length: whatever their bits say, no weight
+      const int left = len - (seg.blk + t0) * kKv4Page;  // tokens from the tile's start
+      if (left < nb * kKv4Page) {
+#pragma unroll
+        for (int b = 0; b < kTile; ++b) {
+          if (b * kKv4Page + row >= left) p[b][0] = p[b][1] = -INFINITY;
+          if (b * kKv4Page + row + 8 >= left) p[b][2] = p[b][3] = -INFINITY;
+        }
+      }
+      // ---- running maximum and sum
+      float alpha[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float mx = fmaxf(p[0][i], p[0][i + 2]);
+#pragma unroll
+        for (int b = 1; b < kTile; ++b) mx = fmaxf(mx, fmaxf(p[b][i], p[b][i + 2]));
+        mx = fmaxf(top[i], rows_max(mx));
+        const float base = mx == -INFINITY ? 0.f : mx;
+        alpha[i] = ex2((top[i] - base) * F[i]);
+        top[i] = mx;
+        const float off = -base * F[i];
+        float s = 0.f;
+#pragma unroll
+        for (int b = 0; b < kTile; ++b) {
+          p[b][i] = ex2(fmaf(p[b][i], F[i], off));
+          p[b][i + 2] = ex2(fmaf(p[b][i + 2], F[i], off));
+          s += p[b][i] + p[b][i + 2];
+        }
+        l[i] = fmaf(l[i], alpha[i], s);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) pm[g][i] *= alpha[i];
+      }
+      // ---- O
+      float acc[NC][2][4], off[NG][4];
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[c][t][i] = 0.f;
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) off[g][i] = 0.f;
+#pragma unroll
+      for (int b = 0; b < kTile; ++b) {
+        if (b < nb) {
+          const int sl = slot + b >= kSlots ? slot + b - kSlots : slot + b;
+          const unsigned char* rec = ring + sl * kRec;
+          uint32_t va[NC], vb[NC], pa[NG], pb[NG];
+          lds<NC>(va, rec + 8 * D + lane * (D / 8));
+          lds<NC>(vb, rec + 12 * D + lane * (D / 8));
+          lds<NG>(pa, rec + 16 * D + (kKv4Page + row) * NG * 4);
+          lds<NG>(pb, rec + 16 * D + (kKv4Page + row + 8) * NG * 4);
+          if (left < (b + 1) * kKv4Page) {
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+              if (b * kKv4Page + row >= left) pa[g] = 0;
+              if (b * kKv4Page + row + 8 >= left) pb[g] = 0;
+            }
+          }
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const float2 sa = pair(pa[g]), sb = pair(pb[g]);
+            pm[g][0] = fmaf(p[b][0], sa.y, fmaf(p[b][2], sb.y, pm[g][0]));
+            pm[g][1] = fmaf(p[b][1], sa.y, fmaf(p[b][3], sb.y, pm[g][1]));
+            const uint32_t b0 = transpose8x8(bf16x2(p[b][0] * sa.x, p[b][1] * sa.x));
+            const uint32_t b1 = transpose8x8(bf16x2(p[b][2] * sb.x, p[b][3] * sb.x));
+            mma_bf16(off[g], 0xc300c300u, 0xc300c300u, 0xc300c300u, 0xc300c300u, b0, b1);
+#pragma unroll
+            for (int c = g * GROUP / 32; c < (g + 1) * GROUP / 32; ++c) {
+              uint32_t a[4], u[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                a[i] = and_or(va[c] >> (4 * i), 0x000f000fu, 0x43004300u);
+                u[i] = and_or(vb[c] >> (4 * i), 0x000f000fu, 0x43004300u);
+              }
+              mma_bf16(acc[c][0], a[0], a[1], u[0], u[1], b0, b1);
+              mma_bf16(acc[c][1], a[2], a[3], u[2], u[3], b0, b1);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            O[c][t][i] = fmaf(O[c][t][i], alpha[i & 1], acc[c][t][i] + off[c * 32 / GROUP][i]);
+      __syncwarp();
+      for (int b = 0; b < nb; ++b) issue();
+      slot = slot + nb >= kSlots ? slot + nb - kSlots : slot + nb;
+    }
+
+    // ---- the piece is done
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] = rows_sum(l[i]);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) pm[g][i] = rows_sum(pm[g][i]);
     }
 #pragma unroll
-    for (int g = 0; g < kMaxG; ++g) {
-      if (g >= P.G) break;
-      float s = 0.f;
+    for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int c = 0; c < kCh; ++c) s = fmaf(q[g][c], k[c], s);
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      s *= P.scale_log2;
-      const float top = fmaxf(mx[g], s), base = top == -INFINITY ? 0.f : top;
-      const float a = exp2f(mx[g] - base), p = exp2f(s - base);
-      mx[g] = top;
-      l[g] = l[g] * a + p;
-#pragma unroll
-      for (int c = 0; c < kCh; ++c) o[g][c] = o[g][c] * a + p * v[c];
+        for (int i = 0; i < 4; ++i) O[c][t][i] += pm[c * 32 / GROUP][i & 1];
+    if (any_bad) {  // a page id outside the pool, somewhere: in this piece?
+      bool bad = false;
+      for (int i = lane; i < n; i += 32) {
+        const int page = __ldg(P.table + (long long)seg.r * P.table_stride + seg.blk + i);
+        bad |= page < 0 || page >= P.pool_blocks;
+      }
+      if (__any_sync(0xffffffffu, bad)) l[0] = l[1] = __int_as_float(0x7fffffff);
     }
-  }
+    const bool starts = seg.blk == 0, ends = seg.blk + n == seg.nblk;
+    if (starts && ends) {
 #pragma unroll
-  for (int g = 0; g < kMaxG; ++g) {
-    sm[w][g] = mx[g];
-    sl[w][g] = l[g];
+      for (int i = 0; i < 2; ++i) {
+        const int g = 2 * j + i;
+        if (g >= G) continue;
+        const float inv = 1.f / l[i];
 #pragma unroll
-    for (int c = 0; c < kCh; ++c) so[w][g][32 * c + lane] = o[g][c];
+        for (int c = 0; c < NC; ++c) {
+          uint2 v;
+          v.x = float_to_row2<FP16>(O[c][0][i] * inv, O[c][0][i + 2] * inv);
+          v.y = float_to_row2<FP16>(O[c][1][i] * inv, O[c][1][i + 2] * inv);
+          *reinterpret_cast<uint2*>(P.o + (orow + g) * D + 32 * c + 4 * row) = v;
+        }
+        if (row == 0) P.lse[orow + g] = fmaf(top[i], F[i] * kLn2, logf(l[i]));
+      }
+    } else {
+      // [0]: its own place; [1] is the warp's last piece: over its ring
+      const int at = starts ? 1 : 0;
+      if (at) {
+        cp_wait<0>();
+        __syncwarp();
+      }
+      float* part = at ? reinterpret_cast<float*>(ring) : part0 + w * G * D;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int g = 2 * j + i;
+        if (g >= G) continue;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          *reinterpret_cast<float4*>(part + g * D + 32 * c + 4 * row) =
+              make_float4(O[c][0][i], O[c][0][i + 2], O[c][1][i], O[c][1][i + 2]);
+        if (row == 0) {
+          float* m2 = ml + ((w * 2 + at) * kMaxG + g) * 2;
+          m2[0] = top[i] * F[i];
+          m2[1] = l[i];
+        }
+      }
+      if (lane == 0) {
+        meta[w].has[at] = 1;
+        if (!at) meta[w].ends0 = ends;
+        meta[w].r[at] = seg.r;
+        meta[w].h[at] = seg.h;
+      }
+    }
+    x += n;
   }
+  cp_wait<0>();
   __syncthreads();
-  for (int i = threadIdx.x; i < P.G * D; i += kWarps * 32) {
-    const int g = i / D, ch = i % D;
-    float top = -INFINITY;
-    for (int x = 0; x < kWarps; ++x) top = fmaxf(top, sm[x][g]);
-    const float base = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, acc = 0.f;
-    for (int x = 0; x < kWarps; ++x) {
-      const float a = exp2f(sm[x][g] - base);
-      sum += sl[x][g] * a;
-      acc += so[x][g][ch] * a;
+
+  // ------------------------------------------------ join the warps' pieces
+  // A run is a piece that begins a segment (or goes on from the CTA before)
+  // and the pieces [0] of the warps behind it up to the segment's end.
+  const auto slot_part = [&](int ww, int at) {
+    return at ? reinterpret_cast<const float*>(smem + ww * S::kRing) : part0 + ww * G * D;
+  };
+  const long long part_stride = (long long)G * D + 2 * kMaxG;
+  int open_w = -1, open_at = 0, sent = 0, sent_r[2], sent_h[2];
+  for (int ww = 0; ww <= kWarps; ++ww) {
+    const bool end = ww == kWarps;
+    bool close = false;
+    int last_w = ww;
+    if (!end && meta[ww].has[0]) {
+      if (open_w < 0) {
+        open_w = ww;
+        open_at = 0;
+      }
+      close = meta[ww].ends0;
     }
-    const float out = len ? acc / sum : 0.f;
-    const long long row = (long long)r * P.H + h * P.G + g;
-    P.o[row * D + ch] = (uint16_t)float_to_row2<FP16>(out, 0.f);
-    if (ch == 0) P.lse[row] = len ? top * 0.69314718055994531f + logf(sum) : -INFINITY;
+    if (end && open_w >= 0) {
+      close = true;
+      last_w = kWarps - 1;
+    }
+    if (close) {
+      const bool starts = open_at == 1, ends = !end;
+      const int r = meta[open_w].r[open_at], h = meta[open_w].h[open_at];
+      const int to = starts ? 1 : 0;
+      float* gp = P.part + ((long long)cta * 2 + to) * part_stride;
+      for (int i = tid; i < G * D; i += kThreads) {
+        const int g = i / D;
+        float mx = ml[((open_w * 2 + open_at) * kMaxG + g) * 2];
+        for (int y = open_w + 1; y <= last_w; ++y)
+          if (meta[y].has[0]) mx = fmaxf(mx, ml[(y * 2 * kMaxG + g) * 2]);
+        const float base = mx == -INFINITY ? 0.f : mx;
+        float sum = 0.f, acc = 0.f;
+        for (int y = open_w; y <= last_w; ++y) {
+          const int at = y == open_w ? open_at : 0;
+          if (!meta[y].has[at]) continue;
+          const float* m2 = ml + ((y * 2 + at) * kMaxG + g) * 2;
+          const float a = ex2(m2[0] - base);
+          sum = fmaf(m2[1], a, sum);
+          acc = fmaf(slot_part(y, at)[i], a, acc);
+        }
+        if (starts && ends) {
+          const long long orow = (long long)r * P.H + (long long)h * G + g;
+          P.o[orow * D + i % D] = (uint16_t)float_to_row2<FP16>(acc / sum, 0.f);
+          if (i % D == 0) P.lse[orow] = mx * kLn2 + logf(sum);
+        } else {
+          gp[i] = acc;
+          if (i % D == 0) {
+            gp[G * D + 2 * g] = mx;
+            gp[G * D + 2 * g + 1] = sum;
+          }
+        }
+      }
+      if (!(starts && ends)) {
+        sent_r[sent] = r;
+        sent_h[sent++] = h;
+      }
+      open_w = -1;
+    }
+    if (!end && meta[ww].has[1]) {
+      open_w = ww;
+      open_at = 1;
+    }
+  }
+
+  // ------------------------------------------------ join the CTAs' parts
+  for (int k = 0; k < sent; ++k) {
+    const int r = sent_r[k], h = sent_h[k], nblk = first[r + 1] - first[r];
+    const long long x0 = (long long)Hk * first[r] + (long long)h * nblk;
+    const int c0 = kv4_worker(W, N, x0), c1 = kv4_worker(W, N, x0 + nblk - 1);
+    __threadfence();
+    __syncthreads();  // all of this CTA's part is written, misc is free again
+    if (tid == 0) {
+      const bool last = atomicAdd(P.counters + c0, 1) == c1 - c0;
+      if (last) P.counters[c0] = 0;  // as the next call finds it
+      misc[0] = last;
+      __threadfence();
+    }
+    __syncthreads();
+    if (!misc[0]) continue;
+    const auto from = [&](int c) {
+      return P.part + ((long long)c * 2 + (c == c0 ? 1 : 0)) * part_stride;
+    };
+    for (int i = tid; i < G * D; i += kThreads) {
+      const int g = i / D;
+      float mx = -INFINITY;
+      for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, __ldcg(from(c) + G * D + 2 * g));
+      const float base = mx == -INFINITY ? 0.f : mx;
+      float sum = 0.f, acc = 0.f;
+      for (int c = c0; c <= c1; ++c) {
+        const float a = ex2(__ldcg(from(c) + G * D + 2 * g) - base);
+        sum = fmaf(__ldcg(from(c) + G * D + 2 * g + 1), a, sum);
+        acc = fmaf(__ldcg(from(c) + i), a, acc);
+      }
+      const long long orow = (long long)r * P.H + (long long)h * G + g;
+      P.o[orow * D + i % D] = (uint16_t)float_to_row2<FP16>(acc / sum, 0.f);
+      if (i % D == 0) P.lse[orow] = mx * kLn2 + logf(sum);
+    }
   }
 }
 
+using Kernel = void (*)(const Kv4Decode);
+
 template <int D, int GROUP>
-cudaError_t decode_of(const Kv4Decode& P, int dtype, cudaStream_t s) {
-  const dim3 grid(P.num_reqs, P.Hk);
-  if (dtype)
-    kv4_decode_kernel<D, GROUP, true><<<grid, kWarps * 32, 0, s>>>(P);
-  else
-    kv4_decode_kernel<D, GROUP, false><<<grid, kWarps * 32, 0, s>>>(P);
-  return cudaGetLastError();
+Kernel kernel_of(int dtype) {
+  return dtype ? kv4_decode_kernel<D, GROUP, true> : kv4_decode_kernel<D, GROUP, false>;
+}
+
+struct Choice {
+  Kernel kernel;
+  int (*smem)(int G, int reqs);
+};
+
+Choice choose(int D, int group, int dtype) {
+  if (D == 64)
+    return group == 32 ? Choice{kernel_of<64, 32>(dtype), Shape<64, 32>::smem}
+                       : Choice{kernel_of<64, 64>(dtype), Shape<64, 64>::smem};
+  if (group == 32) return {kernel_of<128, 32>(dtype), Shape<128, 32>::smem};
+  return group == 64 ? Choice{kernel_of<128, 64>(dtype), Shape<128, 64>::smem}
+                     : Choice{kernel_of<128, 128>(dtype), Shape<128, 128>::smem};
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_decode(const Kv4Decode& P, int D, int group, int dtype, cudaStream_t s) {
-  if (D == 64)
-    return group == 32 ? decode_of<64, 32>(P, dtype, s) : decode_of<64, 64>(P, dtype, s);
-  if (group == 32) return decode_of<128, 32>(P, dtype, s);
-  return group == 64 ? decode_of<128, 64>(P, dtype, s) : decode_of<128, 128>(P, dtype, s);
+  const Choice c = choose(D, group, dtype);
+  // no more CTAs than the tables could give work to
+  const long long most = (long long)P.num_reqs * P.table_stride * P.Hk;
+  const int grid = kv4_workers(most, P.grid, kLeast);
+  c.kernel<<<grid, kThreads, c.smem(P.G, P.num_reqs), s>>>(P);
+  return cudaGetLastError();
 }
 
-cudaError_t kv4_decode_init(int, int, int, int, int* ctas_per_sm, size_t* part_floats) {
-  *ctas_per_sm = 1;
-  *part_floats = 0;
-  return cudaSuccess;
+cudaError_t kv4_decode_init(int D, int group, int dtype, int G, int max_reqs, int* ctas_per_sm,
+                            size_t* part_floats) {
+  const Choice c = choose(D, group, dtype);
+  const int bytes = c.smem(G, max_reqs);
+  *part_floats = 2 * ((size_t)G * D + 2 * kMaxG);
+  cudaError_t e = cudaFuncSetAttribute(c.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       c.smem(kMaxG, kKv4MaxReqs));
+  if (e != cudaSuccess) return e;
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, c.kernel, kThreads, bytes);
 }
 
 }  // namespace pod

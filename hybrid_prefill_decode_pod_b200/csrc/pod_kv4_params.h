@@ -64,7 +64,7 @@ cudaError_t launch_kv4_read(const Kv4Rows& P, int D, int group, int dtype, cudaS
 cudaError_t launch_kv4_decode(const Kv4Decode& P, int D, int group, int dtype, cudaStream_t s);
 // Resident CTAs per SM and workspace floats per CTA of the decode kernel; sets
 // its shared-memory limit on the current device.
-cudaError_t kv4_decode_init(int D, int group, int dtype, int G, int* ctas_per_sm,
+cudaError_t kv4_decode_init(int D, int group, int dtype, int G, int max_reqs, int* ctas_per_sm,
                             size_t* part_floats);
 
 }  // namespace pod

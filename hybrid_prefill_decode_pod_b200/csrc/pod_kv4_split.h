@@ -1,0 +1,54 @@
+// pod_kv4_split.h -- how a decode call's work is cut, shared by the kernel and
+// the host tests.
+//
+// The W = Hk * sum(blocks) blocks of 16 tokens, in the order (request, KV head,
+// block), are one line that N workers cut into equal lengths: worker c takes
+// [c W / N, (c + 1) W / N). A (request, KV head) is a segment of that line and
+// may lie in several workers. With N <= W every worker has a block.
+#pragma once
+
+namespace pod {
+
+#ifdef __CUDACC__
+#define POD_HD __host__ __device__ __forceinline__
+#else
+#define POD_HD inline
+#endif
+
+POD_HD long long kv4_begin(long long W, int N, int c) { return c * W / N; }
+
+// The worker that holds block x: the largest c with c W / N <= x.
+POD_HD int kv4_worker(long long W, int N, long long x) { return (int)(((x + 1) * N - 1) / W); }
+
+// Where block x of the line lies: first[r] is the number of blocks of one head
+// in front of request r (first[R] their sum), 0 <= x < Hk * first[R].
+struct Kv4Place {
+  int r, h, blk, nblk;
+};
+POD_HD Kv4Place kv4_place(const int* first, int R, int Hk, long long x) {
+  const long long v = x / Hk;
+  int lo = 0, hi = R;  // first[lo] <= v < first[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= v)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  Kv4Place p;
+  p.r = lo;
+  p.nblk = first[lo + 1] - first[lo];
+  const long long rem = x - (long long)Hk * first[lo];
+  p.h = (int)(rem / p.nblk);
+  p.blk = (int)(rem - (long long)p.h * p.nblk);
+  return p;
+}
+
+// Workers of a call: no more than there are CTAs, each with at least
+// `least` blocks (one worker where there are fewer).
+POD_HD int kv4_workers(long long W, int ctas, int least) {
+  const long long n = W / least;
+  return n < 1 ? 1 : n < ctas ? (int)n : ctas;
+}
+
+}  // namespace pod

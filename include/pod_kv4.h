@@ -63,7 +63,7 @@ typedef struct pod_kv4_ctx pod_kv4_ctx; /* opaque, library-owned */
 
 typedef struct {
   int num_qo_heads;    /* H (decode only)                                  */
-  int num_kv_heads;    /* Hk; H % Hk == 0                                  */
+  int num_kv_heads;    /* Hk <= 512; H % Hk == 0                           */
   int head_dim;        /* d: 64 or 128                                     */
   int group_size;      /* channels that share a pair (s, m)                */
   int dtype;           /* pod_dtype of Q, K, V, O rows                     */

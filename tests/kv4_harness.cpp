@@ -5,6 +5,7 @@
 // A call that passes its checks then ends at the device (POD_ECUDA where there
 // is none) or at a counting launcher.
 #include "pod_kv4_api.cpp"
+#include "pod_kv4_split.h"
 
 static int g_launches = 0;
 
@@ -13,7 +14,7 @@ cudaError_t launch_qk_norm_rope(const QkParams&, int, int, int, cudaStream_t) { 
 cudaError_t launch_kv4_write(const Kv4Rows&, int, int, int, cudaStream_t) { ++g_launches; return cudaSuccess; }
 cudaError_t launch_kv4_read(const Kv4Rows&, int, int, int, cudaStream_t) { ++g_launches; return cudaSuccess; }
 cudaError_t launch_kv4_decode(const Kv4Decode&, int, int, int, cudaStream_t) { ++g_launches; return cudaSuccess; }
-cudaError_t kv4_decode_init(int, int, int, int, int*, size_t*) { return cudaErrorNotSupported; }
+cudaError_t kv4_decode_init(int, int, int, int, int, int*, size_t*) { return cudaErrorNotSupported; }
 }  // namespace pod
 
 extern "C" {
@@ -22,6 +23,13 @@ POD_API pod_kv4_ctx* harness_ctx(const pod_kv4_config* cfg) {
   pod_kv4_ctx* c = new pod_kv4_ctx();
   c->cfg = *cfg;
   return c;
+}
+POD_API long long harness_begin(long long W, int N, int c) { return kv4_begin(W, N, c); }
+POD_API int harness_worker(long long W, int N, long long x) { return kv4_worker(W, N, x); }
+POD_API int harness_workers(long long W, int ctas, int least) { return kv4_workers(W, ctas, least); }
+POD_API void harness_place(const int* first, int R, int Hk, long long x, int* out) {
+  const Kv4Place p = kv4_place(first, R, Hk, x);
+  out[0] = p.r; out[1] = p.h; out[2] = p.blk; out[3] = p.nblk;
 }
 POD_API void harness_free(pod_kv4_ctx* c) { delete c; }
 }

@@ -177,6 +177,44 @@ def test_norm_rope_refused(harness, kw, code):
     assert rc == code if code is not None else rc in PAST_THE_CHECKS
 
 
+@pytest.mark.parametrize("lens,Hk", [([1], 1), ([0, 5, 0, 0, 17, 1, 0], 3), ([100] * 9, 8), ([4000, 1], 2), ([0, 0, 33], 5)])
+@pytest.mark.parametrize("ctas,least", [(148, 16), (7, 1), (1, 16), (296, 4)])
+def test_work_is_cut_into_equal_whole_parts(harness, lens, Hk, ctas, least):
+    """Every block belongs to one worker, the parts differ by one block, and a block's place is its own."""
+    ll, i32 = ctypes.c_longlong, ctypes.c_int
+    harness.harness_begin.restype = ll
+    harness.harness_begin.argtypes = [ll, i32, i32]
+    harness.harness_worker.argtypes = [ll, i32, ll]
+    harness.harness_workers.argtypes = [ll, i32, i32]
+    harness.harness_place.argtypes = [ctypes.POINTER(i32), i32, i32, ll, ctypes.POINTER(i32)]
+    first = (i32 * (len(lens) + 1))(*[sum(lens[:i]) for i in range(len(lens) + 1)])
+    W = sum(lens) * Hk
+    N = harness.harness_workers(W, ctas, least)
+    assert 1 <= N <= ctas and (N == 1 or W // N >= least)
+    at = [harness.harness_begin(W, N, c) for c in range(N + 1)]
+    assert at[0] == 0 and at[-1] == W and max(b - a for a, b in zip(at, at[1:])) <= W // N + 1
+    want = [(r, h, b, n) for r, n in enumerate(lens) for h in range(Hk) for b in range(n)]
+    out = (i32 * 4)()
+    for x in range(W):
+        c = harness.harness_worker(W, N, x)
+        assert at[c] <= x < at[c + 1]
+        harness.harness_place(first, len(lens), Hk, x, out)
+        assert tuple(out) == want[x]
+
+
+def test_work_of_the_largest_calls(harness):
+    """The products of the cut stay in 64 bits at the largest tables: 2^31 blocks of 512 heads."""
+    ll, i32 = ctypes.c_longlong, ctypes.c_int
+    harness.harness_begin.restype = ll
+    harness.harness_begin.argtypes = [ll, i32, i32]
+    harness.harness_worker.argtypes = [ll, i32, ll]
+    W, N = (2 ** 31 - 1) * 512, 148 * 4
+    for c in (0, 1, 300, N - 1):
+        b = harness.harness_begin(W, N, c)
+        assert b == c * W // N and harness.harness_worker(W, N, b) == c
+        assert c == 0 or harness.harness_worker(W, N, b - 1) == c - 1
+
+
 def test_rope_table_is_exact_far_out():
     t = p4.rope_table(200001, 64, 10000.0, device="cpu")
     assert t.shape == (200001, 64) and t.dtype == torch.float32
