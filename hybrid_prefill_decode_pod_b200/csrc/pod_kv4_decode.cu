@@ -13,93 +13,92 @@
 //    the rows of the product and the G <= 8 heads its columns, so no row is
 //    padding. Each channel group is summed by itself in fp32 and
 //    score = s (sum q n) + m (sum q) joins them.
-//  * V^T p as well: rows are channels, columns heads. Here the weights p s
-//    multiply the codes; they need the exponents of bf16 (in a long context
-//    p s runs below fp16's 2^-14 for tokens that still count together), one
-//    rounding of 2^-8 of each weight, the step of a bf16 output. An AND-OR makes
-//    two bf16 128 + n, and a product with rows of -128 takes the same rounded
-//    weights away again, every 64 tokens, before the sum is long. sum p m is
-//    added in fp32.
+//  * V^T p as well: rows are channels, columns heads, the same subnormals times
+//    the weights p s, rounded to fp16. What the rounding costs is the weight's
+//    error times n - 8, not n: a product with rows of -8 takes eight of each
+//    rounded weight away, sum p (m + 8 s) in fp32 puts them back unrounded. So that those lie high in fp16, each 64
+//    tokens scale them by a power of two that brings the largest s to [2^13,
+//    2^14): a weight is then off by 2^-11 of itself, or by 2^-39 of the largest
+//    possible one where it is below 2^-28 of that (together below 2^-19 of a
+//    million tokens' weight).
 //  * The running maximum and sum, scores, weights and O are fp32; one rescale
 //    every 64 tokens.
 //
 // Work: see pod_kv4_split.h. The line of blocks is cut into equal parts over
 // the CTAs and each of those over its warps, so lengths need no balance and no
-// plan from the host. Warps stream their blocks through rings of their own
-// (cp.async), across segments. What a warp has of a segment that it does not
+// plan from the host. Warps stream their blocks, one bulk copy each, through rings of their
+// own, across segments. What a warp has of a segment that it does not
 // hold whole is joined first in its CTA, then, where the segment leaves the
 // CTA, through the workspace by the CTA that arrives last, in the order of the
 // tokens: the result does not depend on the order of arrival.
 #include "pod_kv4.cuh"
 #include "pod_kv4_split.h"
+#include "pod_plan.h"
+#include "pod_ptx.cuh"
 
 namespace pod {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 12;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 4;   // blocks of 16 tokens between two rescales
-constexpr int kSlots = 8;  // blocks in a warp's ring
+constexpr int kSlots = 6;  // blocks in a warp's ring
 constexpr int kMaxG = 8;
 constexpr int kLeast = 16;  // blocks that make another CTA worth its join
 constexpr float kLn2 = 0.69314718055994531f;
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+// d = a b + c, one 16 x 16 x 8 product
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1, const float (&c)[4]) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "{%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
+        "f"(c[3]));
 }
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{.reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      "fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      "mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// (a & mask) | bits in one instruction
-__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(mask), "r"(bits));
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // N words of shared memory, N = 1, 2 or 4
 template <int N>
-__device__ __forceinline__ void lds(uint32_t (&v)[N], const unsigned char* p) {
-  if constexpr (N == 4) {
-    const uint4 x = *reinterpret_cast<const uint4*>(p);
-    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-  } else if constexpr (N == 2) {
-    const uint2 x = *reinterpret_cast<const uint2*>(p);
-    v[0] = x.x; v[1] = x.y;
-  } else {
-    v[0] = *reinterpret_cast<const uint32_t*>(p);
-  }
+__device__ __forceinline__ void lds(uint32_t (&v)[N], uint32_t at) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at));
+  else
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[0]) : "r"(at));
+}
+// Waits for a phase of a ring slot; gives up after about a second (false).
+__device__ bool slow_wait(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity))
+    if (clock64() - t0 > kDefaultWaitBudget) return false;
+  return true;
 }
 __device__ __forceinline__ float2 pair(uint32_t v) {
   return __half22float2(*reinterpret_cast<__half2*>(&v));
@@ -121,6 +120,7 @@ __device__ __forceinline__ float rows_sum(float x) {
 struct PieceMeta {
   int has[2];  // [0] goes on from the blocks before, [1] begins here and goes on
   int ends0;   // [0] reaches the end of its segment
+  int final0;  // [0] is the warp's last piece
   int r[2], h[2];
 };
 
@@ -129,16 +129,17 @@ struct Shape {
   static constexpr int kRec = kv4_record_bytes(D, GROUP);
   static constexpr int NG = D / GROUP, NC = D / 32;  // channel groups, chunks of 32 channels
   static constexpr int kRing = kSlots * kRec;
-  // shared memory: rings, partial results [warp][G][D] and their (max, sum),
-  // pieces, then the requests' first blocks
+  // V's channels are taken kPart chunks at a time (one channel group at most),
+  // which bounds the accumulators that are live
+  static constexpr int kPart = GROUP >= 64 ? 2 : 1;
+  // shared memory: rings, (max, sum) of the partial results, pieces, then the
+  // requests' first blocks
   static constexpr int kMlOff = kWarps * kRing;  // float [warp][2][kMaxG][2]
   static constexpr int kMetaOff = kMlOff + kWarps * 2 * kMaxG * 2 * 4;
   static constexpr int kMiscOff = kMetaOff + kWarps * (int)sizeof(PieceMeta);
-  static constexpr int kPartOff = (kMiscOff + 64 + 15) / 16 * 16;
-  static __host__ __device__ int part_bytes(int G) { return kWarps * G * D * 4; }
-  static __host__ __device__ int smem(int G, int reqs) {
-    return kPartOff + part_bytes(G) + (reqs + 1) * 4;
-  }
+  static constexpr int kBarOff = (kMiscOff + 64 + 7) / 8 * 8;  // mbarrier [warp][slot]
+  static constexpr int kFirstOff = kBarOff + kWarps * kSlots * 8;
+  static __host__ int smem(int reqs) { return kFirstOff + (reqs + 1) * 4; }
 };
 
 template <int D, int GROUP, bool FP16>
@@ -149,10 +150,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
   float* ml = reinterpret_cast<float*>(smem + S::kMlOff);
   PieceMeta* meta = reinterpret_cast<PieceMeta*>(smem + S::kMetaOff);
   int* misc = reinterpret_cast<int*>(smem + S::kMiscOff);
-  float* part0 = reinterpret_cast<float*>(smem + S::kPartOff);
-  int* first = reinterpret_cast<int*>(smem + S::kPartOff + S::part_bytes(P.G));
+  int* first = reinterpret_cast<int*>(smem + S::kFirstOff);
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, row = lane >> 2, j = lane & 3;
   const int R = P.num_reqs, Hk = P.Hk, G = P.G;
+  const long long part_stride = (long long)G * D + 2 * kMaxG;  // floats of a partial result
+  // the workspace of this CTA: its two parts for other CTAs, then one for each warp
+  float* ws = P.part + blockIdx.x * (2 + kWarps) * part_stride;
   const long long cap = min((long long)P.table_stride * kKv4Page, (1LL << 31) - 16);
   const auto length = [&](int r) { return (int)min((long long)max(__ldg(P.ctx_lens + r), 0), cap); };
 
@@ -169,6 +172,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
     }
     if (lane == 31) misc[w] = inc;
     if (tid < kWarps) meta[tid].has[0] = meta[tid].has[1] = 0;
+    if (tid < kWarps * kSlots) mbar_init(smem_u32(smem + S::kBarOff) + tid * 8, 1);
+    fence_mbar_init();
     __syncthreads();
     int before = inc - sum;
     for (int x = 0; x < w; ++x) before += misc[x];
@@ -197,11 +202,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
   const long long xb = cb + kv4_begin(ce - cb, kWarps, w), xe = cb + kv4_begin(ce - cb, kWarps, w + 1);
   const int total = (int)(xe - xb);
   unsigned char* ring = smem + w * S::kRing;
-  const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring) + lane * 16;
+  const uint32_t ring_s = smem_u32(ring), bar_s = smem_u32(smem + S::kBarOff) + w * kSlots * 8;
 
   // Lane i of `cur` has the record of block 32 b + i, of `nxt` that of the 32
   // behind; -1 where the page id lies outside the pool.
-  bool any_bad = false;
   const auto records = [&](int base) {
     int rec = 0;
     if (base + lane < total) {
@@ -213,31 +217,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
   };
   int cur = records(0), nxt = records(32);
   int issued = 0, islot = 0;
-  const auto issue = [&]() {
-    if (issued < total) {
-      if ((issued & 31) == 0 && issued) {
-        cur = nxt;
-        nxt = records(issued + 32);
-      }
-      const int rec = __shfl_sync(0xffffffffu, cur, issued & 31);
+  bool bad = false;  // this lane met a page id outside the pool
+  // copies the next `count` <= 8 blocks into the slots they follow on, a lane each
+  const auto issue = [&](int count) {
+    const int i = (issued & 31) + lane;
+    const int a = __shfl_sync(0xffffffffu, cur, i & 31), b = __shfl_sync(0xffffffffu, nxt, i & 31);
+    if (lane < count && issued + lane < total) {
+      const int rec = i < 32 ? a : b;
+      const int sl = islot + lane >= kSlots ? islot + lane - kSlots : islot + lane;
       if (rec >= 0) {
-        const unsigned char* src = P.pool + (long long)rec * kRec + lane * 16;
-        const uint32_t dst = ring_s + islot * kRec;
-#pragma unroll
-        for (int i = 0; i < kRec / 512; ++i) cp16(dst + i * 512, src + i * 512);
-        if (kRec % 512 && lane < kRec % 512 / 16)
-          cp16(dst + kRec / 512 * 512, src + kRec / 512 * 512);
+        mbar_expect_tx(bar_s + sl * 8, kRec);
+        bulk_load(ring_s + sl * kRec, P.pool + (long long)rec * kRec, kRec, bar_s + sl * 8);
       } else {
-        any_bad = true;
+        mbar_arrive(bar_s + sl * 8);
+        bad = true;
       }
     }
-    ++issued;
-    islot = islot + 1 == kSlots ? 0 : islot + 1;
-    cp_commit();
+    if ((issued & 31) + count >= 32 && issued < total) {
+      cur = nxt;
+      nxt = records((issued & ~31) + 64);
+    }
+    issued += count;
+    islot = islot + count >= kSlots ? islot + count - kSlots : islot + count;
   };
-  for (int i = 0; i < kSlots; ++i) issue();
+  issue(kSlots);
 
-  int slot = 0;
+  int slot = 0, phase = 0;  // of the next block
+  bool failed = false;
   for (long long x = xb; x < xe;) {
     const Kv4Place seg = kv4_place(first, R, Hk, x);
     const int n = (int)min((long long)(seg.nblk - seg.blk), xe - x);
@@ -296,23 +302,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
       F[1] = __shfl_sync(0xffffffffu, f, 8 * j + 4);
     }
 
-    // State of heads 2 j and 2 j + 1: O of channels 32 c + 4 row + 0..3 (tile t,
-    // rows `row` and `row` + 8 are channels 2 t and 2 t + 1), this lane's part
-    // of the sums of p and of p m.
-    float O[NC][2][4], pm[NG][2], l[2] = {0.f, 0.f}, top[2] = {-INFINITY, -INFINITY};
+    // State of heads 2 j (x) and 2 j + 1 (y): O of channels 32 c + 4 row + 0..3,
+    // this lane's part of the sums of p and of p m.
+    float2 O[NC][4], pm[NG];
+    float l[2] = {0.f, 0.f}, top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int i = 0; i < 4; ++i) O[c][i] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) O[c][t][i] = 0.f;
-#pragma unroll
-    for (int g = 0; g < NG; ++g) pm[g][0] = pm[g][1] = 0.f;
+    for (int g = 0; g < NG; ++g) pm[g] = make_float2(0.f, 0.f);
 
     for (int t0 = 0; t0 < n; t0 += kTile) {
       const int nb = min(kTile, n - t0);
-      cp_wait<kSlots - kTile>();
-      __syncwarp();
+      uint32_t at[kTile];  // the blocks' records
+#pragma unroll
+      for (int b = 0; b < kTile; ++b) {
+        const int wrap = slot + b >= kSlots, sl = slot + b - (wrap ? kSlots : 0);
+        at[b] = ring_s + sl * kRec;
+        if (b < nb && !mbar_try_wait(bar_s + sl * 8, phase ^ wrap) && !failed)
+          failed = !slow_wait(bar_s + sl * 8, phase ^ wrap);
+      }
+      const int left = len - (seg.blk + t0) * kKv4Page;  // tokens from the tile's start
+      if (left < nb * kKv4Page) {
+        // Tokens behind the length get s = m = 0, whatever their bits say.
+        __syncwarp();
+        const uint32_t rec = ring_s + (slot + nb - 1 - (slot + nb > kSlots ? kSlots : 0)) * kRec;
+        const int t = (lane & 15), keep = left - (nb - 1) * kKv4Page;
+        if (t >= keep) {
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(rec + 16 * D + ((lane & 16) + t) * NG * 4 + g * 4), "r"(0) : "memory");
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
       // ---- scores of the tile's tokens: rows `row`, `row` + 8 of each block
       float p[kTile][4];
 #pragma unroll
@@ -320,36 +344,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
 #pragma unroll
         for (int i = 0; i < 4; ++i) p[b][i] = -INFINITY;
         if (b < nb) {
-          const int sl = slot + b >= kSlots ? slot + b - kSlots : slot + b;
-          const unsigned char* rec = ring + sl * kRec;
           uint32_t ka[NC], kb[NC], pa[NG], pb[NG];
-          lds<NC>(ka, rec + lane * (D / 8));
-          lds<NC>(kb, rec + 4 * D + lane * (D / 8));
-          lds<NG>(pa, rec + 16 * D + row * NG * 4);
-          lds<NG>(pb, rec + 16 * D + (row + 8) * NG * 4);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) p[b][i] = 0.f;
+          lds<NC>(ka, at[b] + lane * (D / 8));
+          lds<NC>(kb, at[b] + 4 * D + lane * (D / 8));
+          lds<NG>(pa, at[b] + 16 * D + row * NG * 4);
+          lds<NG>(pb, at[b] + 16 * D + (row + 8) * NG * 4);
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
             float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = g * GROUP / 32; c < (g + 1) * GROUP / 32; ++c) {
-              mma_f16(acc, ka[c] & 0x000f000fu, kb[c] & 0x000f000fu, ka[c] & 0x00f000f0u,
-                      kb[c] & 0x00f000f0u, qf[c][0], qf[c][1]);
+              mma(acc, ka[c] & 0x000f000fu, kb[c] & 0x000f000fu, ka[c] & 0x00f000f0u,
+                  kb[c] & 0x00f000f0u, qf[c][0], qf[c][1], acc);
               const uint32_t a8 = ka[c] >> 8, b8 = kb[c] >> 8;
-              mma_f16(acc, a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u,
-                      b8 & 0x00f000f0u, qf[c][2], qf[c][3]);
+              mma(acc, a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x00f000f0u,
+                  qf[c][2], qf[c][3], acc);
             }
             const float2 sa = pair(pa[g]), sb = pair(pb[g]);
-            p[b][0] = fmaf(sa.x, acc[0], fmaf(sa.y, qs[g][0], p[b][0]));
-            p[b][1] = fmaf(sa.x, acc[1], fmaf(sa.y, qs[g][1], p[b][1]));
-            p[b][2] = fmaf(sb.x, acc[2], fmaf(sb.y, qs[g][0], p[b][2]));
-            p[b][3] = fmaf(sb.x, acc[3], fmaf(sb.y, qs[g][1], p[b][3]));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 sm = i < 2 ? sa : sb;
+              const float mq = g ? fmaf(sm.y, qs[g][i & 1], p[b][i]) : sm.y * qs[g][i & 1];
+              p[b][i] = fmaf(sm.x, acc[i], mq);
+            }
           }
         }
       }
-      // tokens behind the length: whatever their bits say, no weight
-      const int left = len - (seg.blk + t0) * kKv4Page;  // tokens from the tile's start
       if (left < nb * kKv4Page) {
 #pragma unroll
         for (int b = 0; b < kTile; ++b) {
@@ -357,8 +377,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
           if (b * kKv4Page + row + 8 >= left) p[b][2] = p[b][3] = -INFINITY;
         }
       }
-      // ---- running maximum and sum
-      float alpha[2];
+      // ---- the largest scale of the tile's values
+      float up, down;  // 2^k with s 2^k < 2^14, and 2^-k
+      {
+        __half2 big = __half2half2(__ushort_as_half(0));
+#pragma unroll
+        for (int b = 0; b < kTile; ++b) {
+          if (b < nb) {
+            uint32_t pa[NG], pb[NG];
+            lds<NG>(pa, at[b] + 16 * D + (kKv4Page + row) * NG * 4);
+            lds<NG>(pb, at[b] + 16 * D + (kKv4Page + row + 8) * NG * 4);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+              big = __hmax2(big, __habs2(*reinterpret_cast<__half2*>(&pa[g])));
+              big = __hmax2(big, __habs2(*reinterpret_cast<__half2*>(&pb[g])));
+            }
+          }
+        }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) big = __hmax2(big, __shfl_xor_sync(0xffffffffu, big, o));
+        const int e = __float_as_int(__low2float(big)) >> 23;
+        up = e == 0 || e == 255 ? 1.f : __int_as_float((267 - e) << 23);
+        down = e == 0 || e == 255 ? 1.f : __int_as_float((e - 13) << 23);
+      }
+      // ---- running maximum and sum; p becomes 2^k times the weight
+      const float lift = (float)((__float_as_int(up) >> 23) - 127);
+      float2 alpha;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float mx = fmaxf(p[0][i], p[0][i + 2]);
@@ -366,9 +410,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
         for (int b = 1; b < kTile; ++b) mx = fmaxf(mx, fmaxf(p[b][i], p[b][i + 2]));
         mx = fmaxf(top[i], rows_max(mx));
         const float base = mx == -INFINITY ? 0.f : mx;
-        alpha[i] = ex2((top[i] - base) * F[i]);
+        const float a = ex2((top[i] - base) * F[i]);
         top[i] = mx;
-        const float off = -base * F[i];
+        const float off = fmaf(-base, F[i], lift);
         float s = 0.f;
 #pragma unroll
         for (int b = 0; b < kTile; ++b) {
@@ -376,94 +420,95 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
           p[b][i + 2] = ex2(fmaf(p[b][i + 2], F[i], off));
           s += p[b][i] + p[b][i + 2];
         }
-        l[i] = fmaf(l[i], alpha[i], s);
-#pragma unroll
-        for (int g = 0; g < NG; ++g) pm[g][i] *= alpha[i];
+        l[i] = fmaf(l[i], a, s * down);
+        (i ? alpha.y : alpha.x) = a;
       }
-      // ---- O
-      float acc[NC][2][4], off[NG][4];
+      // ---- O, kPart chunks of 32 channels at a time
+      const float2 c24 = make_float2(down * 0x1p24f, down * 0x1p24f);
+      const float2 c20 = make_float2(down * 0x1p20f, down * 0x1p20f);
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
+      for (int g = 0; g < NG; ++g) {
+        uint32_t wt[kTile][2];
+        float2 pmt = make_float2(0.f, 0.f);
+        float off[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[c][t][i] = 0.f;
-#pragma unroll
-      for (int g = 0; g < NG; ++g)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) off[g][i] = 0.f;
-#pragma unroll
-      for (int b = 0; b < kTile; ++b) {
-        if (b < nb) {
-          const int sl = slot + b >= kSlots ? slot + b - kSlots : slot + b;
-          const unsigned char* rec = ring + sl * kRec;
-          uint32_t va[NC], vb[NC], pa[NG], pb[NG];
-          lds<NC>(va, rec + 8 * D + lane * (D / 8));
-          lds<NC>(vb, rec + 12 * D + lane * (D / 8));
-          lds<NG>(pa, rec + 16 * D + (kKv4Page + row) * NG * 4);
-          lds<NG>(pb, rec + 16 * D + (kKv4Page + row + 8) * NG * 4);
-          if (left < (b + 1) * kKv4Page) {
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-              if (b * kKv4Page + row >= left) pa[g] = 0;
-              if (b * kKv4Page + row + 8 >= left) pb[g] = 0;
-            }
-          }
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            const float2 sa = pair(pa[g]), sb = pair(pb[g]);
-            pm[g][0] = fmaf(p[b][0], sa.y, fmaf(p[b][2], sb.y, pm[g][0]));
-            pm[g][1] = fmaf(p[b][1], sa.y, fmaf(p[b][3], sb.y, pm[g][1]));
-            const uint32_t b0 = transpose8x8(bf16x2(p[b][0] * sa.x, p[b][1] * sa.x));
-            const uint32_t b1 = transpose8x8(bf16x2(p[b][2] * sb.x, p[b][3] * sb.x));
-            mma_bf16(off[g], 0xc300c300u, 0xc300c300u, 0xc300c300u, 0xc300c300u, b0, b1);
-#pragma unroll
-            for (int c = g * GROUP / 32; c < (g + 1) * GROUP / 32; ++c) {
-              uint32_t a[4], u[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                a[i] = and_or(va[c] >> (4 * i), 0x000f000fu, 0x43004300u);
-                u[i] = and_or(vb[c] >> (4 * i), 0x000f000fu, 0x43004300u);
-              }
-              mma_bf16(acc[c][0], a[0], a[1], u[0], u[1], b0, b1);
-              mma_bf16(acc[c][1], a[2], a[3], u[2], u[3], b0, b1);
-            }
+        for (int b = 0; b < kTile; ++b) {
+          if (b < nb) {
+            uint32_t pa[1], pb[1];
+            lds<1>(pa, at[b] + 16 * D + (kKv4Page + row) * NG * 4 + g * 4);
+            lds<1>(pb, at[b] + 16 * D + (kKv4Page + row + 8) * NG * 4 + g * 4);
+            const float2 sa = pair(pa[0]), sb = pair(pb[0]);
+            const float ma = fmaf(8.f, sa.x, sa.y), mb = fmaf(8.f, sb.x, sb.y);
+            pmt.x = fmaf(p[b][0], ma, fmaf(p[b][2], mb, pmt.x));
+            pmt.y = fmaf(p[b][1], ma, fmaf(p[b][3], mb, pmt.y));
+            wt[b][0] = transpose8x8(f16x2(p[b][0] * sa.x, p[b][1] * sa.x));
+            wt[b][1] = transpose8x8(f16x2(p[b][2] * sb.x, p[b][3] * sb.x));
+            // -8 2^-24 and -8 2^-20, as the codes of these rows are held
+            mma(off, 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, wt[b][0], wt[b][1], off);
           }
         }
+        pm[g] = fma2(pm[g], alpha, mul2(pmt, make_float2(down, down)));
+#pragma unroll
+        for (int c0 = g * GROUP / 32; c0 < (g + 1) * GROUP / 32; c0 += S::kPart) {
+          float acc[S::kPart][2][4];
+#pragma unroll
+          for (int b = 0; b < kTile; ++b) {
+            if (b < nb) {
+              uint32_t va[S::kPart], vb[S::kPart];
+              lds<S::kPart>(va, at[b] + 8 * D + lane * (D / 8) + c0 * 4);
+              lds<S::kPart>(vb, at[b] + 12 * D + lane * (D / 8) + c0 * 4);
+#pragma unroll
+              for (int c = 0; c < S::kPart; ++c) {
+                mma(acc[c][0], va[c] & 0x000f000fu, va[c] & 0x00f000f0u, vb[c] & 0x000f000fu,
+                    vb[c] & 0x00f000f0u, wt[b][0], wt[b][1], b ? acc[c][0] : off);
+                const uint32_t a8 = va[c] >> 8, b8 = vb[c] >> 8;
+                mma(acc[c][1], a8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x000f000fu,
+                    b8 & 0x00f000f0u, wt[b][0], wt[b][1], b ? acc[c][1] : off);
+              }
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < S::kPart; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 a = make_float2(acc[c][i >> 1][2 * (i & 1)], acc[c][i >> 1][2 * (i & 1) + 1]);
+              O[c0 + c][i] = fma2(a, i & 1 ? c20 : c24, mul2(O[c0 + c][i], alpha));
+            }
+        }
       }
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            O[c][t][i] = fmaf(O[c][t][i], alpha[i & 1], acc[c][t][i] + off[c * 32 / GROUP][i]);
       __syncwarp();
-      for (int b = 0; b < nb; ++b) issue();
-      slot = slot + nb >= kSlots ? slot + nb - kSlots : slot + nb;
+      issue(nb);
+      slot += nb;
+      if (slot >= kSlots) {
+        slot -= kSlots;
+        phase ^= 1;
+      }
     }
 
     // ---- the piece is done
+    l[0] = rows_sum(l[0]);
+    l[1] = rows_sum(l[1]);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] = rows_sum(l[i]);
-#pragma unroll
-      for (int g = 0; g < NG; ++g) pm[g][i] = rows_sum(pm[g][i]);
+    for (int g = 0; g < NG; ++g) {
+      pm[g].x = rows_sum(pm[g].x);
+      pm[g].y = rows_sum(pm[g].y);
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) O[c][t][i] += pm[c * 32 / GROUP][i & 1];
-    if (any_bad) {  // a page id outside the pool, somewhere: in this piece?
-      bool bad = false;
+      for (int i = 0; i < 4; ++i) {
+        O[c][i].x += pm[c * 32 / GROUP].x;
+        O[c][i].y += pm[c * 32 / GROUP].y;
+      }
+    if (__any_sync(0xffffffffu, bad)) {  // a bad page id, somewhere: in this piece?
+      bool here = false;
       for (int i = lane; i < n; i += 32) {
         const int page = __ldg(P.table + (long long)seg.r * P.table_stride + seg.blk + i);
-        bad |= page < 0 || page >= P.pool_blocks;
+        here |= page < 0 || page >= P.pool_blocks;
       }
-      if (__any_sync(0xffffffffu, bad)) l[0] = l[1] = __int_as_float(0x7fffffff);
+      if (__any_sync(0xffffffffu, here)) l[0] = l[1] = __int_as_float(0x7fffffff);
     }
+    if (__any_sync(0xffffffffu, failed)) l[0] = l[1] = __int_as_float(0x7fffffff);
     const bool starts = seg.blk == 0, ends = seg.blk + n == seg.nblk;
     if (starts && ends) {
 #pragma unroll
@@ -473,21 +518,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
         const float inv = 1.f / l[i];
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
+          const auto at = [&](int k) { return (i ? O[c][k].y : O[c][k].x) * inv; };
           uint2 v;
-          v.x = float_to_row2<FP16>(O[c][0][i] * inv, O[c][0][i + 2] * inv);
-          v.y = float_to_row2<FP16>(O[c][1][i] * inv, O[c][1][i + 2] * inv);
+          v.x = float_to_row2<FP16>(at(0), at(1));
+          v.y = float_to_row2<FP16>(at(2), at(3));
           *reinterpret_cast<uint2*>(P.o + (orow + g) * D + 32 * c + 4 * row) = v;
         }
         if (row == 0) P.lse[orow + g] = fmaf(top[i], F[i] * kLn2, logf(l[i]));
       }
     } else {
-      // [0]: its own place; [1] is the warp's last piece: over its ring
-      const int at = starts ? 1 : 0;
-      if (at) {
-        cp_wait<0>();
-        __syncwarp();
-      }
-      float* part = at ? reinterpret_cast<float*>(ring) : part0 + w * G * D;
+      // the warp's last piece lies over its ring, one before others in the workspace
+      const int at = starts ? 1 : 0, final = x + n == xe;
+      if (final) __syncwarp();
+      float* part = final ? reinterpret_cast<float*>(ring) : ws + (2 + w) * part_stride;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int g = 2 * j + i;
@@ -495,7 +538,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
 #pragma unroll
         for (int c = 0; c < NC; ++c)
           *reinterpret_cast<float4*>(part + g * D + 32 * c + 4 * row) =
-              make_float4(O[c][0][i], O[c][0][i + 2], O[c][1][i], O[c][1][i + 2]);
+              i ? make_float4(O[c][0].y, O[c][1].y, O[c][2].y, O[c][3].y)
+                : make_float4(O[c][0].x, O[c][1].x, O[c][2].x, O[c][3].x);
         if (row == 0) {
           float* m2 = ml + ((w * 2 + at) * kMaxG + g) * 2;
           m2[0] = top[i] * F[i];
@@ -504,23 +548,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
       }
       if (lane == 0) {
         meta[w].has[at] = 1;
-        if (!at) meta[w].ends0 = ends;
+        if (!at) {
+          meta[w].ends0 = ends;
+          meta[w].final0 = final;
+        }
         meta[w].r[at] = seg.r;
         meta[w].h[at] = seg.h;
       }
     }
     x += n;
   }
-  cp_wait<0>();
+  // after a wait that ran out: the copies still in flight
+  for (int i = max(total - kSlots, 0); failed && i < total; ++i)
+    slow_wait(bar_s + i % kSlots * 8, i / kSlots & 1);
   __syncthreads();
 
   // ------------------------------------------------ join the warps' pieces
   // A run is a piece that begins a segment (or goes on from the CTA before)
   // and the pieces [0] of the warps behind it up to the segment's end.
   const auto slot_part = [&](int ww, int at) {
-    return at ? reinterpret_cast<const float*>(smem + ww * S::kRing) : part0 + ww * G * D;
+    return at || meta[ww].final0 ? reinterpret_cast<const float*>(smem + ww * S::kRing)
+                                 : ws + (2 + ww) * part_stride;
   };
-  const long long part_stride = (long long)G * D + 2 * kMaxG;
   int open_w = -1, open_at = 0, sent = 0, sent_r[2], sent_h[2];
   for (int ww = 0; ww <= kWarps; ++ww) {
     const bool end = ww == kWarps;
@@ -541,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
       const bool starts = open_at == 1, ends = !end;
       const int r = meta[open_w].r[open_at], h = meta[open_w].h[open_at];
       const int to = starts ? 1 : 0;
-      float* gp = P.part + ((long long)cta * 2 + to) * part_stride;
+      float* gp = ws + to * part_stride;
       for (int i = tid; i < G * D; i += kThreads) {
         const int g = i / D;
         float mx = ml[((open_w * 2 + open_at) * kMaxG + g) * 2];
@@ -597,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
     __syncthreads();
     if (!misc[0]) continue;
     const auto from = [&](int c) {
-      return P.part + ((long long)c * 2 + (c == c0 ? 1 : 0)) * part_stride;
+      return P.part + ((long long)c * (2 + kWarps) + (c == c0 ? 1 : 0)) * part_stride;
     };
     for (int i = tid; i < G * D; i += kThreads) {
       const int g = i / D;
@@ -626,7 +675,7 @@ Kernel kernel_of(int dtype) {
 
 struct Choice {
   Kernel kernel;
-  int (*smem)(int G, int reqs);
+  int (*smem)(int reqs);
 };
 
 Choice choose(int D, int group, int dtype) {
@@ -645,17 +694,17 @@ cudaError_t launch_kv4_decode(const Kv4Decode& P, int D, int group, int dtype, c
   // no more CTAs than the tables could give work to
   const long long most = (long long)P.num_reqs * P.table_stride * P.Hk;
   const int grid = kv4_workers(most, P.grid, kLeast);
-  c.kernel<<<grid, kThreads, c.smem(P.G, P.num_reqs), s>>>(P);
+  c.kernel<<<grid, kThreads, c.smem(P.num_reqs), s>>>(P);
   return cudaGetLastError();
 }
 
 cudaError_t kv4_decode_init(int D, int group, int dtype, int G, int max_reqs, int* ctas_per_sm,
                             size_t* part_floats) {
   const Choice c = choose(D, group, dtype);
-  const int bytes = c.smem(G, max_reqs);
-  *part_floats = 2 * ((size_t)G * D + 2 * kMaxG);
+  const int bytes = c.smem(max_reqs);
+  *part_floats = (2 + kWarps) * ((size_t)G * D + 2 * kMaxG);
   cudaError_t e = cudaFuncSetAttribute(c.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       c.smem(kMaxG, kKv4MaxReqs));
+                                       c.smem(kKv4MaxReqs));
   if (e != cudaSuccess) return e;
   return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, c.kernel, kThreads, bytes);
 }

@@ -26,7 +26,8 @@ struct Kv4Place {
   int r, h, blk, nblk;
 };
 POD_HD Kv4Place kv4_place(const int* first, int R, int Hk, long long x) {
-  const long long v = x / Hk;
+  const bool small = x < (1LL << 31);  // 32-bit divisions take a third of the time
+  const int v = small ? (int)((unsigned)x / (unsigned)Hk) : (int)(x / Hk);
   int lo = 0, hi = R;  // first[lo] <= v < first[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -39,7 +40,7 @@ POD_HD Kv4Place kv4_place(const int* first, int R, int Hk, long long x) {
   p.r = lo;
   p.nblk = first[lo + 1] - first[lo];
   const long long rem = x - (long long)Hk * first[lo];
-  p.h = (int)(rem / p.nblk);
+  p.h = small ? (int)((unsigned)rem / (unsigned)p.nblk) : (int)(rem / p.nblk);
   p.blk = (int)(rem - (long long)p.h * p.nblk);
   return p;
 }

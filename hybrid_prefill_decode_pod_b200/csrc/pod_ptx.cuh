@@ -85,6 +85,15 @@ POD_DEV void tma_load_3d_hint(uint32_t dst, const CUtensorMap* map, uint32_t bar
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
       : "memory");
 }
+// Untiled copy global -> shared by the TMA unit: both addresses and the size
+// are multiples of 16 bytes.
+POD_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
 // 16-byte asynchronous copy global -> shared through L1-bypassing loads
 // (cp.async.cg); completion is tracked per thread with commit groups.
 POD_DEV void cp_async16(uint32_t dst, const void* src) {

@@ -57,17 +57,18 @@ def quantised(x, group):
 
 def attend(q, records, table, lens, d, group, *, keys=None):
     """O, LSE in fp64 of q [R, H, d] over the pool `records` [blocks, Hk, bytes], and the
-    parts of an error bound: E[s n], E|v - o|, and the largest sum |q_i k_i| / sqrt(d)."""
+    parts of an error bound: E[s |n - 8|], E[16 s], E|v - o|, and the largest sum |q_i k_i| / sqrt(d)."""
     R, H, _ = q.shape
     Hk = records.shape[1]
-    o, spread, dev = (torch.zeros(R, H, d, dtype=torch.float64) for _ in range(3))
+    o, spread, wide, dev = (torch.zeros(R, H, d, dtype=torch.float64) for _ in range(4))
     lse, big = torch.full((R, H), -math.inf, dtype=torch.float64), torch.zeros(R, H, dtype=torch.float64)
     for r, n in enumerate(lens):
         if n == 0:
             continue
         code, s, m = unpack(records[table[r, :-(-n // PAGE)].long()], d, group)
         val = (code * s + m).permute(2, 1, 0, 3, 4).flatten(2, 3)[:, :, :n]   # 2, Hk, n, d
-        above = (code * s).permute(2, 1, 0, 3, 4).flatten(2, 3)[1, :, :n]
+        near = ((code - 8).abs() * s).permute(2, 1, 0, 3, 4).flatten(2, 3)[1, :, :n]
+        step = (16 * s).permute(2, 1, 0, 3, 4).flatten(2, 3)[1, :, :n]
         for h in range(H):
             g = h // (H // Hk)
             k, v = val[0, g], val[1, g]
@@ -77,23 +78,23 @@ def attend(q, records, table, lens, d, group, *, keys=None):
             lse[r, h] = torch.logsumexp(sc, 0)
             p = torch.softmax(sc, 0)
             o[r, h] = p @ v
-            spread[r, h] = p @ above[g]
+            spread[r, h], wide[r, h] = p @ near[g], p @ step[g]
             dev[r, h] = p @ (v - o[r, h]).abs()
-    return o, lse, (spread, dev, big)
+    return o, lse, (spread, wide, dev, big)
 
 
 def attend_bounds(o, lse, parts, dtype):
     """How far the kernel's O and LSE may be from the exact ones.
 
-    Each weight p s is rounded once to bf16 (half a step: 2^-8 of it), which moves O by at most
-    2^-8 E[s n]. A score carries the fp32 roundings of d products and sums (below 2^-17 of
+    Each weight p s is rounded once to fp16 (half a step: 2^-11 of it), which moves O by at most
+    2^-11 E[s |n - 8|]. A score carries the fp32 roundings of d products and sums (below 2^-17 of
     sum |q_i k_i| for d <= 128, 128 roundings of 2^-24 each) and moves O by twice that times
-    E|v - o|, LSE by once. fp32 sums over the keys add at most 2^-13 of E[s n] + |o|, in parts of
-    64 keys whose sums are held with the codes raised by 128 (their 17 / 2 times larger values).
+    E|v - o|, LSE by once. The fp32 products and sums over the keys (of codes up to 16 s, then of
+    the parts) add below 2^-16 of E[16 s] + |o|: a hundred roundings of 2^-23 and as much again.
     The output is rounded once."""
-    spread, dev, big = parts
+    spread, wide, dev, big = parts
     score = big.unsqueeze(-1) * 2.0 ** -17
-    bound = 2.0 ** -8 * spread + 2 * score * dev + 2.0 ** -13 * (spread + o.abs())
+    bound = 2.0 ** -11 * spread + 2 * score * dev + 2.0 ** -16 * (wide + o.abs())
     bound = bound + EPS[dtype] / 2 * (o.abs() + bound) + 2.0 ** -24
     return bound, big * 2.0 ** -17 + 2.0 ** -20 * (1 + lse.abs().nan_to_num(0, 0, 0))
 
