@@ -138,7 +138,9 @@ struct Shape {
   static constexpr int kMetaOff = kMlOff + kWarps * 2 * kMaxG * 2 * 4;
   static constexpr int kMiscOff = kMetaOff + kWarps * (int)sizeof(PieceMeta);
   static constexpr int kBarOff = (kMiscOff + 64 + 7) / 8 * 8;  // mbarrier [warp][slot]
-  static constexpr int kFirstOff = kBarOff + kWarps * kSlots * 8;
+  // a record whose pairs are 0, for a tile of fewer than kTile blocks
+  static constexpr int kZeroOff = (kBarOff + kWarps * kSlots * 8 + 15) / 16 * 16;
+  static constexpr int kFirstOff = kZeroOff + kRec;
   static __host__ int smem(int reqs) { return kFirstOff + (reqs + 1) * 4; }
 };
 
@@ -174,6 +176,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
     if (tid < kWarps) meta[tid].has[0] = meta[tid].has[1] = 0;
     if (tid < kWarps * kSlots) mbar_init(smem_u32(smem + S::kBarOff) + tid * 8, 1);
     fence_mbar_init();
+    for (int i = tid; i < kRec / 4; i += kThreads)
+      reinterpret_cast<uint32_t*>(smem + S::kZeroOff)[i] = 0;
     __syncthreads();
     int before = inc - sum;
     for (int x = 0; x < w; ++x) before += misc[x];
@@ -202,7 +206,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
   const long long xb = cb + kv4_begin(ce - cb, kWarps, w), xe = cb + kv4_begin(ce - cb, kWarps, w + 1);
   const int total = (int)(xe - xb);
   unsigned char* ring = smem + w * S::kRing;
-  const uint32_t ring_s = smem_u32(ring), bar_s = smem_u32(smem + S::kBarOff) + w * kSlots * 8;
+  const uint32_t ring_s = smem_u32(ring), bar_s = smem_u32(smem + S::kBarOff) + w * kSlots * 8,
+                 zero_s = smem_u32(smem + S::kZeroOff);
 
   // Lane i of `cur` has the record of block 32 b + i, of `nxt` that of the 32
   // behind; -1 where the page id lies outside the pool.
@@ -315,62 +320,76 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
 
     for (int t0 = 0; t0 < n; t0 += kTile) {
       const int nb = min(kTile, n - t0);
-      uint32_t at[kTile];  // the blocks' records
+      // The blocks' records. A tile of fewer than kTile blocks takes the zero
+      // record instead, so that all of the tile's work is one run of
+      // independent instructions.
+      uint32_t at[kTile];
 #pragma unroll
       for (int b = 0; b < kTile; ++b) {
         const int wrap = slot + b >= kSlots, sl = slot + b - (wrap ? kSlots : 0);
-        at[b] = ring_s + sl * kRec;
+        at[b] = b < nb ? ring_s + sl * kRec : zero_s;
         if (b < nb && !mbar_try_wait(bar_s + sl * 8, phase ^ wrap) && !failed)
           failed = !slow_wait(bar_s + sl * 8, phase ^ wrap);
       }
-      const int left = len - (seg.blk + t0) * kKv4Page;  // tokens from the tile's start
-      if (left < nb * kKv4Page) {
+      // tokens of the tile
+      const int left = min(len - (seg.blk + t0) * kKv4Page, nb * kKv4Page);
+      if (left & 15) {
         // Tokens behind the length get s = m = 0, whatever their bits say.
         __syncwarp();
         const uint32_t rec = ring_s + (slot + nb - 1 - (slot + nb > kSlots ? kSlots : 0)) * kRec;
-        const int t = (lane & 15), keep = left - (nb - 1) * kKv4Page;
-        if (t >= keep) {
+        if ((lane & 15) >= (left & 15)) {
 #pragma unroll
           for (int g = 0; g < NG; ++g)
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(rec + 16 * D + ((lane & 16) + t) * NG * 4 + g * 4), "r"(0) : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(rec + 16 * D + lane * NG * 4 + g * 4), "r"(0) : "memory");
         }
         fence_proxy_async_smem();
         __syncwarp();
       }
       // ---- scores of the tile's tokens: rows `row`, `row` + 8 of each block
       float p[kTile][4];
+      {
+        uint32_t ka[kTile][NC], kb[kTile][NC];
 #pragma unroll
-      for (int b = 0; b < kTile; ++b) {
+        for (int b = 0; b < kTile; ++b) {
+          lds<NC>(ka[b], at[b] + lane * (D / 8));
+          lds<NC>(kb[b], at[b] + 4 * D + lane * (D / 8));
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[b][i] = -INFINITY;
-        if (b < nb) {
-          uint32_t ka[NC], kb[NC], pa[NG], pb[NG];
-          lds<NC>(ka, at[b] + lane * (D / 8));
-          lds<NC>(kb, at[b] + 4 * D + lane * (D / 8));
-          lds<NG>(pa, at[b] + 16 * D + row * NG * 4);
-          lds<NG>(pb, at[b] + 16 * D + (row + 8) * NG * 4);
+        for (int g = 0; g < NG; ++g) {
+          float acc[kTile][4];
 #pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int b = 0; b < kTile; ++b)
 #pragma unroll
-            for (int c = g * GROUP / 32; c < (g + 1) * GROUP / 32; ++c) {
-              mma(acc, ka[c] & 0x000f000fu, kb[c] & 0x000f000fu, ka[c] & 0x00f000f0u,
-                  kb[c] & 0x00f000f0u, qf[c][0], qf[c][1], acc);
-              const uint32_t a8 = ka[c] >> 8, b8 = kb[c] >> 8;
-              mma(acc, a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x00f000f0u,
-                  qf[c][2], qf[c][3], acc);
+            for (int i = 0; i < 4; ++i) acc[b][i] = 0.f;
+#pragma unroll
+          for (int c = g * GROUP / 32; c < (g + 1) * GROUP / 32; ++c) {
+#pragma unroll
+            for (int b = 0; b < kTile; ++b)
+              mma(acc[b], ka[b][c] & 0x000f000fu, kb[b][c] & 0x000f000fu, ka[b][c] & 0x00f000f0u,
+                  kb[b][c] & 0x00f000f0u, qf[c][0], qf[c][1], acc[b]);
+#pragma unroll
+            for (int b = 0; b < kTile; ++b) {
+              const uint32_t a8 = ka[b][c] >> 8, b8 = kb[b][c] >> 8;
+              mma(acc[b], a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x00f000f0u,
+                  qf[c][2], qf[c][3], acc[b]);
             }
-            const float2 sa = pair(pa[g]), sb = pair(pb[g]);
+          }
+#pragma unroll
+          for (int b = 0; b < kTile; ++b) {
+            uint32_t pa[1], pb[1];
+            lds<1>(pa, at[b] + 16 * D + row * NG * 4 + g * 4);
+            lds<1>(pb, at[b] + 16 * D + (row + 8) * NG * 4 + g * 4);
+            const float2 sa = pair(pa[0]), sb = pair(pb[0]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float2 sm = i < 2 ? sa : sb;
               const float mq = g ? fmaf(sm.y, qs[g][i & 1], p[b][i]) : sm.y * qs[g][i & 1];
-              p[b][i] = fmaf(sm.x, acc[i], mq);
+              p[b][i] = fmaf(sm.x, acc[b][i], mq);
             }
           }
         }
       }
-      if (left < nb * kKv4Page) {
+      if (left < kTile * kKv4Page) {
 #pragma unroll
         for (int b = 0; b < kTile; ++b) {
           if (b * kKv4Page + row >= left) p[b][0] = p[b][1] = -INFINITY;
@@ -383,15 +402,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
         __half2 big = __half2half2(__ushort_as_half(0));
 #pragma unroll
         for (int b = 0; b < kTile; ++b) {
-          if (b < nb) {
-            uint32_t pa[NG], pb[NG];
-            lds<NG>(pa, at[b] + 16 * D + (kKv4Page + row) * NG * 4);
-            lds<NG>(pb, at[b] + 16 * D + (kKv4Page + row + 8) * NG * 4);
+          uint32_t pa[NG], pb[NG];
+          lds<NG>(pa, at[b] + 16 * D + (kKv4Page + row) * NG * 4);
+          lds<NG>(pb, at[b] + 16 * D + (kKv4Page + row + 8) * NG * 4);
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-              big = __hmax2(big, __habs2(*reinterpret_cast<__half2*>(&pa[g])));
-              big = __hmax2(big, __habs2(*reinterpret_cast<__half2*>(&pb[g])));
-            }
+          for (int g = 0; g < NG; ++g) {
+            big = __hmax2(big, __habs2(*reinterpret_cast<__half2*>(&pa[g])));
+            big = __hmax2(big, __habs2(*reinterpret_cast<__half2*>(&pb[g])));
           }
         }
 #pragma unroll
@@ -433,38 +450,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
         float off[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int b = 0; b < kTile; ++b) {
-          if (b < nb) {
-            uint32_t pa[1], pb[1];
-            lds<1>(pa, at[b] + 16 * D + (kKv4Page + row) * NG * 4 + g * 4);
-            lds<1>(pb, at[b] + 16 * D + (kKv4Page + row + 8) * NG * 4 + g * 4);
-            const float2 sa = pair(pa[0]), sb = pair(pb[0]);
-            const float ma = fmaf(8.f, sa.x, sa.y), mb = fmaf(8.f, sb.x, sb.y);
-            pmt.x = fmaf(p[b][0], ma, fmaf(p[b][2], mb, pmt.x));
-            pmt.y = fmaf(p[b][1], ma, fmaf(p[b][3], mb, pmt.y));
-            wt[b][0] = transpose8x8(f16x2(p[b][0] * sa.x, p[b][1] * sa.x));
-            wt[b][1] = transpose8x8(f16x2(p[b][2] * sb.x, p[b][3] * sb.x));
-            // -8 2^-24 and -8 2^-20, as the codes of these rows are held
-            mma(off, 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, wt[b][0], wt[b][1], off);
-          }
+          uint32_t pa[1], pb[1];
+          lds<1>(pa, at[b] + 16 * D + (kKv4Page + row) * NG * 4 + g * 4);
+          lds<1>(pb, at[b] + 16 * D + (kKv4Page + row + 8) * NG * 4 + g * 4);
+          const float2 sa = pair(pa[0]), sb = pair(pb[0]);
+          const float ma = fmaf(8.f, sa.x, sa.y), mb = fmaf(8.f, sb.x, sb.y);
+          pmt.x = fmaf(p[b][0], ma, fmaf(p[b][2], mb, pmt.x));
+          pmt.y = fmaf(p[b][1], ma, fmaf(p[b][3], mb, pmt.y));
+          wt[b][0] = transpose8x8(f16x2(p[b][0] * sa.x, p[b][1] * sa.x));
+          wt[b][1] = transpose8x8(f16x2(p[b][2] * sb.x, p[b][3] * sb.x));
         }
+        // -8 2^-24 and -8 2^-20, as the codes of these rows are held
+#pragma unroll
+        for (int b = 0; b < kTile; ++b)
+          mma(off, 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, wt[b][0], wt[b][1], off);
         pm[g] = fma2(pm[g], alpha, mul2(pmt, make_float2(down, down)));
 #pragma unroll
         for (int c0 = g * GROUP / 32; c0 < (g + 1) * GROUP / 32; c0 += S::kPart) {
           float acc[S::kPart][2][4];
 #pragma unroll
           for (int b = 0; b < kTile; ++b) {
-            if (b < nb) {
-              uint32_t va[S::kPart], vb[S::kPart];
-              lds<S::kPart>(va, at[b] + 8 * D + lane * (D / 8) + c0 * 4);
-              lds<S::kPart>(vb, at[b] + 12 * D + lane * (D / 8) + c0 * 4);
+            uint32_t va[S::kPart], vb[S::kPart];
+            lds<S::kPart>(va, at[b] + 8 * D + lane * (D / 8) + c0 * 4);
+            lds<S::kPart>(vb, at[b] + 12 * D + lane * (D / 8) + c0 * 4);
 #pragma unroll
-              for (int c = 0; c < S::kPart; ++c) {
-                mma(acc[c][0], va[c] & 0x000f000fu, va[c] & 0x00f000f0u, vb[c] & 0x000f000fu,
-                    vb[c] & 0x00f000f0u, wt[b][0], wt[b][1], b ? acc[c][0] : off);
-                const uint32_t a8 = va[c] >> 8, b8 = vb[c] >> 8;
-                mma(acc[c][1], a8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x000f000fu,
-                    b8 & 0x00f000f0u, wt[b][0], wt[b][1], b ? acc[c][1] : off);
-              }
+            for (int c = 0; c < S::kPart; ++c) {
+              mma(acc[c][0], va[c] & 0x000f000fu, va[c] & 0x00f000f0u, vb[c] & 0x000f000fu,
+                  vb[c] & 0x00f000f0u, wt[b][0], wt[b][1], b ? acc[c][0] : off);
+              const uint32_t a8 = va[c] >> 8, b8 = vb[c] >> 8;
+              mma(acc[c][1], a8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x000f000fu,
+                  b8 & 0x00f000f0u, wt[b][0], wt[b][1], b ? acc[c][1] : off);
             }
           }
 #pragma unroll
@@ -564,104 +579,129 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
   __syncthreads();
 
   // ------------------------------------------------ join the warps' pieces
-  // A run is a piece that begins a segment (or goes on from the CTA before)
-  // and the pieces [0] of the warps behind it up to the segment's end.
-  const auto slot_part = [&](int ww, int at) {
-    return at || meta[ww].final0 ? reinterpret_cast<const float*>(smem + ww * S::kRing)
-                                 : ws + (2 + ww) * part_stride;
+  // A run is a piece that begins a segment (or goes on from the CTA before) and
+  // the pieces [0] of the warps behind it up to the segment's end. The warps of
+  // a run join it together, each a share of its channels.
+  const bool is_warp = lane < kWarps;
+  const uint32_t has0 = __ballot_sync(0xffffffffu, is_warp && meta[lane].has[0]);
+  const uint32_t has1 = __ballot_sync(0xffffffffu, is_warp && meta[lane].has[1]);
+  const uint32_t ends0 = __ballot_sync(0xffffffffu, is_warp && meta[lane].has[0] && meta[lane].ends0);
+  const auto piece_of = [&](int y, int at) {
+    return at || meta[y].final0 ? reinterpret_cast<const float*>(smem + y * S::kRing)
+                                : ws + (2 + y) * part_stride;
   };
-  int open_w = -1, open_at = 0, sent = 0, sent_r[2], sent_h[2];
-  for (int ww = 0; ww <= kWarps; ++ww) {
-    const bool end = ww == kWarps;
-    bool close = false;
-    int last_w = ww;
-    if (!end && meta[ww].has[0]) {
-      if (open_w < 0) {
-        open_w = ww;
-        open_at = 0;
+#pragma unroll
+  for (int at = 0; at < 2; ++at) {
+    if (!((at ? has1 : has0) >> w & 1)) continue;
+    const uint32_t below = has1 & ((1u << w) - 1);
+    const int from = at ? w : below ? 31 - __clz(below) : __ffs(has0) - 1;
+    const int from_at = at || below ? 1 : 0;
+    const uint32_t done = ends0 >> w >> at << at << w;  // ends at this warp (at = 0) or behind it
+    const bool ends = done != 0, starts = from_at == 1;
+    const uint32_t reach = has0 & ~((2u << from) - 1);
+    const int to = ends ? __ffs(done) - 1 : reach ? 31 - __clz(reach) : from;
+    // (a CTA of few blocks has warps without any among them)
+    const uint32_t members = (1u << from) | (reach & ((2u << to) - 1));
+    const int r = meta[w].r[at], h = meta[w].h[at];
+    float* gp = ws + (starts ? 1 : 0) * part_stride;
+    for (int i = __popc(members & ((1u << w) - 1)) * 32 + lane; i < G * D / 4;
+         i += __popc(members) * 32) {
+      const int g = i / (D / 4);
+      float mx = -INFINITY;
+      for (uint32_t m = members; m; m &= m - 1) {
+        const int y = __ffs(m) - 1;
+        mx = fmaxf(mx, ml[((y * 2 + (y == from ? from_at : 0)) * kMaxG + g) * 2]);
       }
-      close = meta[ww].ends0;
-    }
-    if (end && open_w >= 0) {
-      close = true;
-      last_w = kWarps - 1;
-    }
-    if (close) {
-      const bool starts = open_at == 1, ends = !end;
-      const int r = meta[open_w].r[open_at], h = meta[open_w].h[open_at];
-      const int to = starts ? 1 : 0;
-      float* gp = ws + to * part_stride;
-      for (int i = tid; i < G * D; i += kThreads) {
-        const int g = i / D;
-        float mx = ml[((open_w * 2 + open_at) * kMaxG + g) * 2];
-        for (int y = open_w + 1; y <= last_w; ++y)
-          if (meta[y].has[0]) mx = fmaxf(mx, ml[(y * 2 * kMaxG + g) * 2]);
-        const float base = mx == -INFINITY ? 0.f : mx;
-        float sum = 0.f, acc = 0.f;
-        for (int y = open_w; y <= last_w; ++y) {
-          const int at = y == open_w ? open_at : 0;
-          if (!meta[y].has[at]) continue;
-          const float* m2 = ml + ((y * 2 + at) * kMaxG + g) * 2;
-          const float a = ex2(m2[0] - base);
-          sum = fmaf(m2[1], a, sum);
-          acc = fmaf(slot_part(y, at)[i], a, acc);
-        }
-        if (starts && ends) {
-          const long long orow = (long long)r * P.H + (long long)h * G + g;
-          P.o[orow * D + i % D] = (uint16_t)float_to_row2<FP16>(acc / sum, 0.f);
-          if (i % D == 0) P.lse[orow] = mx * kLn2 + logf(sum);
-        } else {
-          gp[i] = acc;
-          if (i % D == 0) {
-            gp[G * D + 2 * g] = mx;
-            gp[G * D + 2 * g + 1] = sum;
-          }
-        }
+      const float base = mx == -INFINITY ? 0.f : mx;
+      float sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (uint32_t m = members; m; m &= m - 1) {
+        const int y = __ffs(m) - 1, y_at = y == from ? from_at : 0;
+        const float* m2 = ml + ((y * 2 + y_at) * kMaxG + g) * 2;
+        const float e = ex2(m2[0] - base);
+        const float4 v = reinterpret_cast<const float4*>(piece_of(y, y_at))[i];
+        sum = fmaf(m2[1], e, sum);
+        acc.x = fmaf(v.x, e, acc.x);
+        acc.y = fmaf(v.y, e, acc.y);
+        acc.z = fmaf(v.z, e, acc.z);
+        acc.w = fmaf(v.w, e, acc.w);
       }
-      if (!(starts && ends)) {
-        sent_r[sent] = r;
-        sent_h[sent++] = h;
+      if (starts && ends) {
+        const long long orow = (long long)r * P.H + (long long)h * G + g;
+        const float inv = 1.f / sum;
+        uint2 v;
+        v.x = float_to_row2<FP16>(acc.x * inv, acc.y * inv);
+        v.y = float_to_row2<FP16>(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2*>(P.o + orow * D + i % (D / 4) * 4) = v;
+        if (i % (D / 4) == 0) P.lse[orow] = mx * kLn2 + logf(sum);
+      } else {
+        reinterpret_cast<float4*>(gp)[i] = acc;
+        if (i % (D / 4) == 0)
+          *reinterpret_cast<float2*>(gp + G * D + 2 * g) = make_float2(mx, sum);
       }
-      open_w = -1;
-    }
-    if (!end && meta[ww].has[1]) {
-      open_w = ww;
-      open_at = 1;
     }
   }
 
   // ------------------------------------------------ join the CTAs' parts
-  for (int k = 0; k < sent; ++k) {
-    const int r = sent_r[k], h = sent_h[k], nblk = first[r + 1] - first[r];
-    const long long x0 = (long long)Hk * first[r] + (long long)h * nblk;
-    const int c0 = kv4_worker(W, N, x0), c1 = kv4_worker(W, N, x0 + nblk - 1);
-    __threadfence();
-    __syncthreads();  // all of this CTA's part is written, misc is free again
-    if (tid == 0) {
-      const bool last = atomicAdd(P.counters + c0, 1) == c1 - c0;
-      if (last) P.counters[c0] = 0;  // as the next call finds it
-      misc[0] = last;
-      __threadfence();
+  // Those are the CTA's first segment, if it does not begin here or goes on, and
+  // its last, if it goes on.
+  const Kv4Place head = kv4_place(first, R, Hk, cb), tail = kv4_place(first, R, Hk, ce - 1);
+  const bool tail_out = tail.blk + 1 < tail.nblk;
+  const bool head_out = head.blk > 0, same = head.r == tail.r && head.h == tail.h;
+  if (!head_out && !tail_out) return;
+  __threadfence();
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const Kv4Place seg = k ? tail : head;
+    const long long x0 = (long long)Hk * first[seg.r] + (long long)seg.h * seg.nblk;
+    const int c0 = kv4_worker(W, N, x0), c1 = kv4_worker(W, N, x0 + seg.nblk - 1);
+    if (tid == k * 32) {
+      bool last = false;
+      if (k ? tail_out && !(same && head_out) : head_out) {
+        last = atomicAdd(P.counters + c0, 1) == c1 - c0;
+        if (last) P.counters[c0] = 0;  // as the next call finds it
+        __threadfence();
+      }
+      misc[k] = last;
     }
-    __syncthreads();
-    if (!misc[0]) continue;
-    const auto from = [&](int c) {
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (!misc[k]) continue;
+    const Kv4Place seg = k ? tail : head;
+    const long long x0 = (long long)Hk * first[seg.r] + (long long)seg.h * seg.nblk;
+    const int c0 = kv4_worker(W, N, x0), c1 = kv4_worker(W, N, x0 + seg.nblk - 1);
+    const auto part_of = [&](int c) {
       return P.part + ((long long)c * (2 + kWarps) + (c == c0 ? 1 : 0)) * part_stride;
     };
-    for (int i = tid; i < G * D; i += kThreads) {
-      const int g = i / D;
+    for (int i = tid; i < G * D / 4; i += kThreads) {
+      const int g = i / (D / 4);
       float mx = -INFINITY;
-      for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, __ldcg(from(c) + G * D + 2 * g));
+#pragma unroll 4
+      for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, __ldcg(part_of(c) + G * D + 2 * g));
       const float base = mx == -INFINITY ? 0.f : mx;
-      float sum = 0.f, acc = 0.f;
+      float sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
       for (int c = c0; c <= c1; ++c) {
-        const float a = ex2(__ldcg(from(c) + G * D + 2 * g) - base);
-        sum = fmaf(__ldcg(from(c) + G * D + 2 * g + 1), a, sum);
-        acc = fmaf(__ldcg(from(c) + i), a, acc);
+        const float2 m2 = __ldcg(reinterpret_cast<const float2*>(part_of(c) + G * D + 2 * g));
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of(c)) + i);
+        const float e = ex2(m2.x - base);
+        sum = fmaf(m2.y, e, sum);
+        acc.x = fmaf(v.x, e, acc.x);
+        acc.y = fmaf(v.y, e, acc.y);
+        acc.z = fmaf(v.z, e, acc.z);
+        acc.w = fmaf(v.w, e, acc.w);
       }
-      const long long orow = (long long)r * P.H + (long long)h * G + g;
-      P.o[orow * D + i % D] = (uint16_t)float_to_row2<FP16>(acc / sum, 0.f);
-      if (i % D == 0) P.lse[orow] = mx * kLn2 + logf(sum);
+      const long long orow = (long long)seg.r * P.H + (long long)seg.h * G + g;
+      const float inv = 1.f / sum;
+      uint2 v;
+      v.x = float_to_row2<FP16>(acc.x * inv, acc.y * inv);
+      v.y = float_to_row2<FP16>(acc.z * inv, acc.w * inv);
+      *reinterpret_cast<uint2*>(P.o + orow * D + i % (D / 4) * 4) = v;
+      if (i % (D / 4) == 0) P.lse[orow] = mx * kLn2 + logf(sum);
     }
   }
 }
