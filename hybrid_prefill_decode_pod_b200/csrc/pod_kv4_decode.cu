@@ -129,9 +129,7 @@ struct Shape {
   static constexpr int kRec = kv4_record_bytes(D, GROUP);
   static constexpr int NG = D / GROUP, NC = D / 32;  // channel groups, chunks of 32 channels
   static constexpr int kRing = kSlots * kRec;
-  // V's channels are taken kPart chunks at a time (one channel group at most),
-  // which bounds the accumulators that are live
-  static constexpr int kPart = GROUP >= 64 ? 2 : 1;
+  static constexpr int CG = GROUP / 32;  // chunks of a group
   // shared memory: rings, (max, sum) of the partial results, pieces, then the
   // requests' first blocks
   static constexpr int kMlOff = kWarps * kRing;  // float [warp][2][kMaxG][2]
@@ -144,16 +142,25 @@ struct Shape {
   static __host__ int smem(int reqs) { return kFirstOff + (reqs + 1) * 4; }
 };
 
-template <int D, int GROUP, bool FP16>
+// REP: how often each head stands among the eight columns of the products
+// (columns REP of them apart, 8 / REP heads at most). With REP > 1 a column
+// takes every REP-th channel group only: its queries are 0 in the others, so one
+// accumulator holds REP groups' sums, the pairs (s, m) of REP groups are applied
+// by one instruction, and REP groups' weights are one operand.
+template <int D, int GROUP, bool FP16, int REP>
 __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode P) {
   using S = Shape<D, GROUP>;
-  constexpr int NG = S::NG, NC = S::NC, kRec = S::kRec;
+  constexpr int NG = S::NG, NC = S::NC, CG = S::CG, kRec = S::kRec;
+  constexpr int NP = NG / REP;           // passes over the groups
+  constexpr int kPart = REP > 1 || CG == 1 ? 1 : 2;  // chunks of a group at a time in V^T p
   extern __shared__ __align__(128) unsigned char smem[];
   float* ml = reinterpret_cast<float*>(smem + S::kMlOff);
   PieceMeta* meta = reinterpret_cast<PieceMeta*>(smem + S::kMetaOff);
   int* misc = reinterpret_cast<int*>(smem + S::kMiscOff);
   int* first = reinterpret_cast<int*>(smem + S::kFirstOff);
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, row = lane >> 2, j = lane & 3;
+  // the replica and the heads of this lane's columns 2 j and 2 j + 1
+  const int rep = REP == 1 ? 0 : REP == 2 ? j >> 1 : j, head0 = 2 * j % (8 / REP);
   const int R = P.num_reqs, Hk = P.Hk, G = P.G;
   const long long part_stride = (long long)G * D + 2 * kMaxG;  // floats of a partial result
   // the workspace of this CTA: its two parts for other CTAs, then one for each warp
@@ -258,14 +265,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
     // The queries as the second operand: column `row` is a head, chunk c's
     // channels 32 c + 8 j + i in the order in which K's codes come apart.
     uint32_t qf[NC][4];
-    float qs[NG][2], F[2];
+    float qs[NP][2], F[2];
     {
+      const int q_head = row % (8 / REP), q_rep = row / (8 / REP);
       float q[NC][8], big = 0.f;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (row < G)
-          v = __ldg(reinterpret_cast<const uint4*>(P.q + (orow + row) * D + 32 * c + 8 * j));
+        if (q_head < G)
+          v = __ldg(reinterpret_cast<const uint4*>(P.q + (orow + q_head) * D + 32 * c + 8 * j));
         const uint32_t vv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -281,15 +289,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
       const int e = __float_as_int(big) >> 23;
       const float sc = e == 0 || e == 255 ? 1.f : __int_as_float(min(263 - e, 254) << 23);
       const float f = P.scale_log2 * 16777216.f / sc;
-      float sum[NG];
+      float sum[NP];
 #pragma unroll
-      for (int g = 0; g < NG; ++g) sum[g] = 0.f;
+      for (int u = 0; u < NP; ++u) sum[u] = 0.f;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
+        const bool own = c / CG % REP == q_rep;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          q[c][i] *= sc;
-          sum[c * 32 / GROUP] += q[c][i];
+          q[c][i] = own ? q[c][i] * sc : 0.f;
+          sum[c / CG / REP] += q[c][i];
         }
         qf[c][0] = float_to_row2<true>(q[c][0], q[c][4]);
         qf[c][1] = float_to_row2<true>(q[c][1] * 0.0625f, q[c][5] * 0.0625f);
@@ -297,26 +306,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
         qf[c][3] = float_to_row2<true>(q[c][3] * 0.0625f, q[c][7] * 0.0625f);
       }
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
-        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
-        qs[g][0] = __shfl_sync(0xffffffffu, sum[g], 8 * j) * 0x1p-24f;
-        qs[g][1] = __shfl_sync(0xffffffffu, sum[g], 8 * j + 4) * 0x1p-24f;
+      for (int u = 0; u < NP; ++u) {
+        sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], 1);
+        sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], 2);
+        qs[u][0] = __shfl_sync(0xffffffffu, sum[u], 8 * j) * 0x1p-24f;
+        qs[u][1] = __shfl_sync(0xffffffffu, sum[u], 8 * j + 4) * 0x1p-24f;
       }
       F[0] = __shfl_sync(0xffffffffu, f, 8 * j);
       F[1] = __shfl_sync(0xffffffffu, f, 8 * j + 4);
     }
 
-    // State of heads 2 j (x) and 2 j + 1 (y): O of channels 32 c + 4 row + 0..3,
-    // this lane's part of the sums of p and of p m.
-    float2 O[NC][4], pm[NG];
+    // State of heads head0 (x) and head0 + 1 (y): O of channels 4 row + 0..3 of the
+    // own groups' chunks, this lane's part of the sums of p and of p (m + 8 s).
+    float2 O[NC / REP][4], pm[NP];
     float l[2] = {0.f, 0.f}, top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+    for (int c = 0; c < NC / REP; ++c)
 #pragma unroll
       for (int i = 0; i < 4; ++i) O[c][i] = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int g = 0; g < NG; ++g) pm[g] = make_float2(0.f, 0.f);
+    for (int g = 0; g < NP; ++g) pm[g] = make_float2(0.f, 0.f);
 
     for (int t0 = 0; t0 < n; t0 += kTile) {
       const int nb = min(kTile, n - t0);
@@ -355,14 +364,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
           lds<NC>(kb[b], at[b] + 4 * D + lane * (D / 8));
         }
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
+        for (int u = 0; u < NP; ++u) {
           float acc[kTile][4];
 #pragma unroll
           for (int b = 0; b < kTile; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[b][i] = 0.f;
 #pragma unroll
-          for (int c = g * GROUP / 32; c < (g + 1) * GROUP / 32; ++c) {
+          for (int c = u * REP * CG; c < (u + 1) * REP * CG; ++c) {
 #pragma unroll
             for (int b = 0; b < kTile; ++b)
               mma(acc[b], ka[b][c] & 0x000f000fu, kb[b][c] & 0x000f000fu, ka[b][c] & 0x00f000f0u,
@@ -377,16 +386,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
 #pragma unroll
           for (int b = 0; b < kTile; ++b) {
             uint32_t pa[1], pb[1];
-            lds<1>(pa, at[b] + 16 * D + row * NG * 4 + g * 4);
-            lds<1>(pb, at[b] + 16 * D + (row + 8) * NG * 4 + g * 4);
+            lds<1>(pa, at[b] + 16 * D + (row * NG + u * REP + rep) * 4);
+            lds<1>(pb, at[b] + 16 * D + ((row + 8) * NG + u * REP + rep) * 4);
             const float2 sa = pair(pa[0]), sb = pair(pb[0]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float2 sm = i < 2 ? sa : sb;
-              const float mq = g ? fmaf(sm.y, qs[g][i & 1], p[b][i]) : sm.y * qs[g][i & 1];
+              const float mq = u ? fmaf(sm.y, qs[u][i & 1], p[b][i]) : sm.y * qs[u][i & 1];
               p[b][i] = fmaf(sm.x, acc[b][i], mq);
             }
           }
+        }
+        if (REP > 1) {
+#pragma unroll
+          for (int b = 0; b < kTile; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (REP == 4) p[b][i] += __shfl_xor_sync(0xffffffffu, p[b][i], 1);
+              p[b][i] += __shfl_xor_sync(0xffffffffu, p[b][i], 2);
+            }
         }
       }
       if (left < kTile * kKv4Page) {
@@ -402,17 +420,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
         __half2 big = __half2half2(__ushort_as_half(0));
 #pragma unroll
         for (int b = 0; b < kTile; ++b) {
-          uint32_t pa[NG], pb[NG];
-          lds<NG>(pa, at[b] + 16 * D + (kKv4Page + row) * NG * 4);
-          lds<NG>(pb, at[b] + 16 * D + (kKv4Page + row + 8) * NG * 4);
 #pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            big = __hmax2(big, __habs2(*reinterpret_cast<__half2*>(&pa[g])));
-            big = __hmax2(big, __habs2(*reinterpret_cast<__half2*>(&pb[g])));
+          for (int u = 0; u < NP; ++u) {
+            uint32_t pa[1], pb[1];
+            lds<1>(pa, at[b] + 16 * D + ((kKv4Page + row) * NG + u * REP + rep) * 4);
+            lds<1>(pb, at[b] + 16 * D + ((kKv4Page + row + 8) * NG + u * REP + rep) * 4);
+            big = __hmax2(big, __habs2(*reinterpret_cast<__half2*>(&pa[0])));
+            big = __hmax2(big, __habs2(*reinterpret_cast<__half2*>(&pb[0])));
           }
         }
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) big = __hmax2(big, __shfl_xor_sync(0xffffffffu, big, o));
+        for (int o = REP == 1 ? 4 : 4 / REP; o < 32; o <<= 1)
+          big = __hmax2(big, __shfl_xor_sync(0xffffffffu, big, o));
         const int e = __float_as_int(__low2float(big)) >> 23;
         up = e == 0 || e == 255 ? 1.f : __int_as_float((267 - e) << 23);
         down = e == 0 || e == 255 ? 1.f : __int_as_float((e - 13) << 23);
@@ -440,19 +459,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
         l[i] = fmaf(l[i], a, s * down);
         (i ? alpha.y : alpha.x) = a;
       }
-      // ---- O, kPart chunks of 32 channels at a time
+      // ---- O
       const float2 c24 = make_float2(down * 0x1p24f, down * 0x1p24f);
       const float2 c20 = make_float2(down * 0x1p20f, down * 0x1p20f);
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
+      for (int u = 0; u < NP; ++u) {
         uint32_t wt[kTile][2];
         float2 pmt = make_float2(0.f, 0.f);
         float off[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int b = 0; b < kTile; ++b) {
           uint32_t pa[1], pb[1];
-          lds<1>(pa, at[b] + 16 * D + (kKv4Page + row) * NG * 4 + g * 4);
-          lds<1>(pb, at[b] + 16 * D + (kKv4Page + row + 8) * NG * 4 + g * 4);
+          lds<1>(pa, at[b] + 16 * D + ((kKv4Page + row) * NG + u * REP + rep) * 4);
+          lds<1>(pb, at[b] + 16 * D + ((kKv4Page + row + 8) * NG + u * REP + rep) * 4);
           const float2 sa = pair(pa[0]), sb = pair(pb[0]);
           const float ma = fmaf(8.f, sa.x, sa.y), mb = fmaf(8.f, sb.x, sb.y);
           pmt.x = fmaf(p[b][0], ma, fmaf(p[b][2], mb, pmt.x));
@@ -464,30 +483,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
 #pragma unroll
         for (int b = 0; b < kTile; ++b)
           mma(off, 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, wt[b][0], wt[b][1], off);
-        pm[g] = fma2(pm[g], alpha, mul2(pmt, make_float2(down, down)));
+        pm[u] = fma2(pm[u], alpha, mul2(pmt, make_float2(down, down)));
+        // chunks c0 .. of each of the pass's groups; a column's own group counts
 #pragma unroll
-        for (int c0 = g * GROUP / 32; c0 < (g + 1) * GROUP / 32; c0 += S::kPart) {
-          float acc[S::kPart][2][4];
+        for (int c0 = 0; c0 < CG; c0 += kPart) {
+          float acc[REP * kPart][2][4];
 #pragma unroll
           for (int b = 0; b < kTile; ++b) {
-            uint32_t va[S::kPart], vb[S::kPart];
-            lds<S::kPart>(va, at[b] + 8 * D + lane * (D / 8) + c0 * 4);
-            lds<S::kPart>(vb, at[b] + 12 * D + lane * (D / 8) + c0 * 4);
 #pragma unroll
-            for (int c = 0; c < S::kPart; ++c) {
-              mma(acc[c][0], va[c] & 0x000f000fu, va[c] & 0x00f000f0u, vb[c] & 0x000f000fu,
-                  vb[c] & 0x00f000f0u, wt[b][0], wt[b][1], b ? acc[c][0] : off);
-              const uint32_t a8 = va[c] >> 8, b8 = vb[c] >> 8;
-              mma(acc[c][1], a8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x000f000fu,
-                  b8 & 0x00f000f0u, wt[b][0], wt[b][1], b ? acc[c][1] : off);
+            for (int y = 0; y < REP; ++y) {
+              const int chunk = (u * REP + y) * CG + c0;
+              uint32_t va[kPart], vb[kPart];
+              lds<kPart>(va, at[b] + 8 * D + lane * (D / 8) + chunk * 4);
+              lds<kPart>(vb, at[b] + 12 * D + lane * (D / 8) + chunk * 4);
+#pragma unroll
+              for (int c = 0; c < kPart; ++c) {
+                float(&lo)[4] = acc[y * kPart + c][0], (&hi)[4] = acc[y * kPart + c][1];
+                mma(lo, va[c] & 0x000f000fu, va[c] & 0x00f000f0u, vb[c] & 0x000f000fu,
+                    vb[c] & 0x00f000f0u, wt[b][0], wt[b][1], b ? lo : off);
+                const uint32_t a8 = va[c] >> 8, b8 = vb[c] >> 8;
+                mma(hi, a8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x000f000fu, b8 & 0x00f000f0u,
+                    wt[b][0], wt[b][1], b ? hi : off);
+              }
             }
           }
 #pragma unroll
-          for (int c = 0; c < S::kPart; ++c)
+          for (int c = 0; c < kPart; ++c)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float2 a = make_float2(acc[c][i >> 1][2 * (i & 1)], acc[c][i >> 1][2 * (i & 1) + 1]);
-              O[c0 + c][i] = fma2(a, i & 1 ? c20 : c24, mul2(O[c0 + c][i], alpha));
+              float2 a = make_float2(acc[c][i >> 1][2 * (i & 1)], acc[c][i >> 1][2 * (i & 1) + 1]);
+#pragma unroll
+              for (int y = 1; y < REP; ++y) {
+                a.x = rep == y ? acc[y][i >> 1][2 * (i & 1)] : a.x;
+                a.y = rep == y ? acc[y][i >> 1][2 * (i & 1) + 1] : a.y;
+              }
+              float2& o = O[u * CG + c0 + c][i];
+              o = fma2(a, i & 1 ? c20 : c24, mul2(o, alpha));
             }
         }
       }
@@ -504,17 +535,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
     l[0] = rows_sum(l[0]);
     l[1] = rows_sum(l[1]);
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      pm[g].x = rows_sum(pm[g].x);
-      pm[g].y = rows_sum(pm[g].y);
+    for (int u = 0; u < NP; ++u) {
+      pm[u].x = rows_sum(pm[u].x);
+      pm[u].y = rows_sum(pm[u].y);
     }
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+    for (int c = 0; c < NC / REP; ++c)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        O[c][i].x += pm[c * 32 / GROUP].x;
-        O[c][i].y += pm[c * 32 / GROUP].y;
+        O[c][i].x += pm[c / CG].x;
+        O[c][i].y += pm[c / CG].y;
       }
+    // where chunk c of O lies among the head's channels
+    const auto channel = [&](int c) { return 32 * ((c / CG * REP + rep) * CG + c % CG) + 4 * row; };
     if (__any_sync(0xffffffffu, bad)) {  // a bad page id, somewhere: in this piece?
       bool here = false;
       for (int i = lane; i < n; i += 32) {
@@ -528,18 +561,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
     if (starts && ends) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int g = 2 * j + i;
+        const int g = head0 + i;
         if (g >= G) continue;
         const float inv = 1.f / l[i];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
+        for (int c = 0; c < NC / REP; ++c) {
           const auto at = [&](int k) { return (i ? O[c][k].y : O[c][k].x) * inv; };
           uint2 v;
           v.x = float_to_row2<FP16>(at(0), at(1));
           v.y = float_to_row2<FP16>(at(2), at(3));
-          *reinterpret_cast<uint2*>(P.o + (orow + g) * D + 32 * c + 4 * row) = v;
+          *reinterpret_cast<uint2*>(P.o + (orow + g) * D + channel(c)) = v;
         }
-        if (row == 0) P.lse[orow + g] = fmaf(top[i], F[i] * kLn2, logf(l[i]));
+        if (row == 0 && rep == 0) P.lse[orow + g] = fmaf(top[i], F[i] * kLn2, logf(l[i]));
       }
     } else {
       // the warp's last piece lies over its ring, one before others in the workspace
@@ -548,14 +581,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
       float* part = final ? reinterpret_cast<float*>(ring) : ws + (2 + w) * part_stride;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int g = 2 * j + i;
+        const int g = head0 + i;
         if (g >= G) continue;
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-          *reinterpret_cast<float4*>(part + g * D + 32 * c + 4 * row) =
+        for (int c = 0; c < NC / REP; ++c)
+          *reinterpret_cast<float4*>(part + g * D + channel(c)) =
               i ? make_float4(O[c][0].y, O[c][1].y, O[c][2].y, O[c][3].y)
                 : make_float4(O[c][0].x, O[c][1].x, O[c][2].x, O[c][3].x);
-        if (row == 0) {
+        if (row == 0 && rep == 0) {
           float* m2 = ml + ((w * 2 + at) * kMaxG + g) * 2;
           m2[0] = top[i] * F[i];
           m2[1] = l[i];
@@ -708,29 +741,38 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
 
 using Kernel = void (*)(const Kv4Decode);
 
-template <int D, int GROUP>
-Kernel kernel_of(int dtype) {
-  return dtype ? kv4_decode_kernel<D, GROUP, true> : kv4_decode_kernel<D, GROUP, false>;
-}
-
 struct Choice {
   Kernel kernel;
   int (*smem)(int reqs);
 };
 
-Choice choose(int D, int group, int dtype) {
-  if (D == 64)
-    return group == 32 ? Choice{kernel_of<64, 32>(dtype), Shape<64, 32>::smem}
-                       : Choice{kernel_of<64, 64>(dtype), Shape<64, 64>::smem};
-  if (group == 32) return {kernel_of<128, 32>(dtype), Shape<128, 32>::smem};
-  return group == 64 ? Choice{kernel_of<128, 64>(dtype), Shape<128, 64>::smem}
-                     : Choice{kernel_of<128, 128>(dtype), Shape<128, 128>::smem};
+template <int D, int GROUP, int REP>
+Choice of(int dtype) {
+  return {dtype ? kv4_decode_kernel<D, GROUP, true, REP> : kv4_decode_kernel<D, GROUP, false, REP>,
+          Shape<D, GROUP>::smem};
+}
+
+// As many replicas as there is room for beside the heads, at most one a group.
+template <int D, int GROUP>
+Choice choose_rep(int dtype, int G) {
+  constexpr int NG = D / GROUP;
+  if constexpr (NG >= 4)
+    if (G <= 2) return of<D, GROUP, 4>(dtype);
+  if constexpr (NG >= 2)
+    if (G <= 4) return of<D, GROUP, 2>(dtype);
+  return of<D, GROUP, 1>(dtype);
+}
+
+Choice choose(int D, int group, int dtype, int G) {
+  if (D == 64) return group == 32 ? choose_rep<64, 32>(dtype, G) : choose_rep<64, 64>(dtype, G);
+  if (group == 32) return choose_rep<128, 32>(dtype, G);
+  return group == 64 ? choose_rep<128, 64>(dtype, G) : choose_rep<128, 128>(dtype, G);
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_decode(const Kv4Decode& P, int D, int group, int dtype, cudaStream_t s) {
-  const Choice c = choose(D, group, dtype);
+  const Choice c = choose(D, group, dtype, P.G);
   // no more CTAs than the tables could give work to
   const long long most = (long long)P.num_reqs * P.table_stride * P.Hk;
   const int grid = kv4_workers(most, P.grid, kLeast);
@@ -740,7 +782,7 @@ cudaError_t launch_kv4_decode(const Kv4Decode& P, int D, int group, int dtype, c
 
 cudaError_t kv4_decode_init(int D, int group, int dtype, int G, int max_reqs, int* ctas_per_sm,
                             size_t* part_floats) {
-  const Choice c = choose(D, group, dtype);
+  const Choice c = choose(D, group, dtype, G);
   const int bytes = c.smem(max_reqs);
   *part_floats = (2 + kWarps) * ((size_t)G * D + 2 * kMaxG);
   cudaError_t e = cudaFuncSetAttribute(c.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
