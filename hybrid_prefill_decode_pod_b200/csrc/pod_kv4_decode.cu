@@ -93,6 +93,20 @@ __device__ __forceinline__ void lds(uint32_t (&v)[N], uint32_t at) {
   else
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[0]) : "r"(at));
 }
+// The pairs of every REP-th group
+template <int NP, int REP>
+__device__ __forceinline__ void own_pairs(uint32_t (&v)[NP], uint32_t at) {
+  if constexpr (REP == 1) {
+    lds<NP>(v, at);
+  } else {
+#pragma unroll
+    for (int u = 0; u < NP; ++u) {
+      uint32_t x[1];
+      lds<1>(x, at + u * REP * 4);
+      v[u] = x[0];
+    }
+  }
+}
 // Waits for a phase of a ring slot; gives up after about a second (false).
 __device__ bool slow_wait(uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
@@ -100,6 +114,8 @@ __device__ bool slow_wait(uint32_t bar, uint32_t parity) {
     if (clock64() - t0 > kDefaultWaitBudget) return false;
   return true;
 }
+// The upper bytes of both halves
+__device__ __forceinline__ uint32_t high_bytes(uint32_t v) { return __byte_perm(v, 0, 0x4341); }
 __device__ __forceinline__ float2 pair(uint32_t v) {
   return __half22float2(*reinterpret_cast<__half2*>(&v));
 }
@@ -124,6 +140,13 @@ struct PieceMeta {
   int r[2], h[2];
 };
 
+// A segment that other CTAs hold parts of: this CTA's first (which does not begin
+// here or goes on), or its last (which begins here and goes on). c0 .. c1 are
+// the CTAs; c0 = c1 where there is none.
+struct Shared {
+  int r, h, c0, c1;
+};
+
 template <int D, int GROUP>
 struct Shape {
   static constexpr int kRec = kv4_record_bytes(D, GROUP);
@@ -135,7 +158,7 @@ struct Shape {
   static constexpr int kMlOff = kWarps * kRing;  // float [warp][2][kMaxG][2]
   static constexpr int kMetaOff = kMlOff + kWarps * 2 * kMaxG * 2 * 4;
   static constexpr int kMiscOff = kMetaOff + kWarps * (int)sizeof(PieceMeta);
-  static constexpr int kBarOff = (kMiscOff + 64 + 7) / 8 * 8;  // mbarrier [warp][slot]
+  static constexpr int kBarOff = (kMiscOff + 2 * kWarps * 4 + 2 * (int)sizeof(Shared) + 7) / 8 * 8;  // mbarrier [warp][slot]
   // a record whose pairs are 0, for a tile of fewer than kTile blocks
   static constexpr int kZeroOff = (kBarOff + kWarps * kSlots * 8 + 15) / 16 * 16;
   static constexpr int kFirstOff = kZeroOff + kRec;
@@ -157,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
   float* ml = reinterpret_cast<float*>(smem + S::kMlOff);
   PieceMeta* meta = reinterpret_cast<PieceMeta*>(smem + S::kMetaOff);
   int* misc = reinterpret_cast<int*>(smem + S::kMiscOff);
+  Shared* out = reinterpret_cast<Shared*>(misc + 2 * kWarps);
   int* first = reinterpret_cast<int*>(smem + S::kFirstOff);
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, row = lane >> 2, j = lane & 3;
   // the replica and the heads of this lane's columns 2 j and 2 j + 1
@@ -230,13 +254,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
   int cur = records(0), nxt = records(32);
   int issued = 0, islot = 0;
   bool bad = false;  // this lane met a page id outside the pool
-  // copies the next `count` <= 8 blocks into the slots they follow on, a lane each
+  // Copies the next `count` blocks into the slots they follow on: block i by lane
+  // i % 32, which holds its record.
   const auto issue = [&](int count) {
-    const int i = (issued & 31) + lane;
-    const int a = __shfl_sync(0xffffffffu, cur, i & 31), b = __shfl_sync(0xffffffffu, nxt, i & 31);
-    if (lane < count && issued + lane < total) {
-      const int rec = i < 32 ? a : b;
-      const int sl = islot + lane >= kSlots ? islot + lane - kSlots : islot + lane;
+    const int d = (lane - issued) & 31;
+    if (d < count && issued + d < total) {
+      const int rec = (issued & 31) + d < 32 ? cur : nxt;
+      const int sl = islot + d >= kSlots ? islot + d - kSlots : islot + d;
       if (rec >= 0) {
         mbar_expect_tx(bar_s + sl * 8, kRec);
         bulk_load(ring_s + sl * kRec, P.pool + (long long)rec * kRec, kRec, bar_s + sl * 8);
@@ -253,6 +277,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
     islot = islot + count >= kSlots ? islot + count - kSlots : islot + count;
   };
   issue(kSlots);
+
+  // what the CTA's ends share with others, while the first blocks are on their way
+  if (lane == 0 && w < 2) {
+    const Kv4Place p = kv4_place(first, R, Hk, w ? ce - 1 : cb);
+    const long long x0 = (long long)Hk * first[p.r] + (long long)p.h * p.nblk;
+    Shared m{p.r, p.h, 0, 0};
+    if (w ? x0 >= cb && x0 + p.nblk > ce : x0 < cb) {
+      m.c0 = kv4_worker(W, N, x0);
+      m.c1 = kv4_worker(W, N, x0 + p.nblk - 1);
+    }
+    out[w] = m;
+  }
 
   int slot = 0, phase = 0;  // of the next block
   bool failed = false;
@@ -329,16 +365,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
 
     for (int t0 = 0; t0 < n; t0 += kTile) {
       const int nb = min(kTile, n - t0);
+      // lane b waits for the tile's block b
+      {
+        const int sl = slot + lane;
+        const uint32_t bar = bar_s + (sl >= kSlots ? sl - kSlots : sl) * 8;
+        const uint32_t parity = phase ^ (sl >= kSlots);
+        if (lane < nb && !mbar_try_wait(bar, parity) && !failed) failed = !slow_wait(bar, parity);
+        __syncwarp();
+      }
       // The blocks' records. A tile of fewer than kTile blocks takes the zero
       // record instead, so that all of the tile's work is one run of
       // independent instructions.
       uint32_t at[kTile];
 #pragma unroll
       for (int b = 0; b < kTile; ++b) {
-        const int wrap = slot + b >= kSlots, sl = slot + b - (wrap ? kSlots : 0);
-        at[b] = b < nb ? ring_s + sl * kRec : zero_s;
-        if (b < nb && !mbar_try_wait(bar_s + sl * 8, phase ^ wrap) && !failed)
-          failed = !slow_wait(bar_s + sl * 8, phase ^ wrap);
+        at[b] = ring_s + slot * kRec + b * kRec;
+        if (slot + b >= kSlots) at[b] -= kSlots * kRec;
+      }
+      if (nb < kTile) {
+#pragma unroll
+        for (int b = 1; b < kTile; ++b)
+          if (b >= nb) at[b] = zero_s;
       }
       // tokens of the tile
       const int left = min(len - (seg.blk + t0) * kKv4Page, nb * kKv4Page);
@@ -357,9 +404,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
       // ---- scores of the tile's tokens: rows `row`, `row` + 8 of each block
       float p[kTile][4];
       {
-        uint32_t ka[kTile][NC], kb[kTile][NC];
+        uint32_t ka[kTile][NC], kb[kTile][NC], kp[kTile][2][NP];
 #pragma unroll
         for (int b = 0; b < kTile; ++b) {
+          own_pairs<NP, REP>(kp[b][0], at[b] + 16 * D + (row * NG + rep) * 4);
+          own_pairs<NP, REP>(kp[b][1], at[b] + 16 * D + ((row + 8) * NG + rep) * 4);
           lds<NC>(ka[b], at[b] + lane * (D / 8));
           lds<NC>(kb[b], at[b] + 4 * D + lane * (D / 8));
         }
@@ -385,10 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
           }
 #pragma unroll
           for (int b = 0; b < kTile; ++b) {
-            uint32_t pa[1], pb[1];
-            lds<1>(pa, at[b] + 16 * D + (row * NG + u * REP + rep) * 4);
-            lds<1>(pb, at[b] + 16 * D + ((row + 8) * NG + u * REP + rep) * 4);
-            const float2 sa = pair(pa[0]), sb = pair(pb[0]);
+            const float2 sa = pair(kp[b][0][u]), sb = pair(kp[b][1][u]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float2 sm = i < 2 ? sa : sb;
@@ -416,17 +462,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
       }
       // ---- the largest scale of the tile's values
       float up, down;  // 2^k with s 2^k < 2^14, and 2^-k
+      uint32_t vp[kTile][2][NP];  // V's pairs of the own groups
       {
         __half2 big = __half2half2(__ushort_as_half(0));
 #pragma unroll
         for (int b = 0; b < kTile; ++b) {
 #pragma unroll
-          for (int u = 0; u < NP; ++u) {
-            uint32_t pa[1], pb[1];
-            lds<1>(pa, at[b] + 16 * D + ((kKv4Page + row) * NG + u * REP + rep) * 4);
-            lds<1>(pb, at[b] + 16 * D + ((kKv4Page + row + 8) * NG + u * REP + rep) * 4);
-            big = __hmax2(big, __habs2(*reinterpret_cast<__half2*>(&pa[0])));
-            big = __hmax2(big, __habs2(*reinterpret_cast<__half2*>(&pb[0])));
+          for (int y = 0; y < 2; ++y) {
+            own_pairs<NP, REP>(vp[b][y], at[b] + 16 * D + ((kKv4Page + row + 8 * y) * NG + rep) * 4);
+#pragma unroll
+            for (int u = 0; u < NP; ++u)
+              big = __hmax2(big, __habs2(*reinterpret_cast<__half2*>(&vp[b][y][u])));
           }
         }
 #pragma unroll
@@ -469,20 +515,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
         float off[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int b = 0; b < kTile; ++b) {
-          uint32_t pa[1], pb[1];
-          lds<1>(pa, at[b] + 16 * D + ((kKv4Page + row) * NG + u * REP + rep) * 4);
-          lds<1>(pb, at[b] + 16 * D + ((kKv4Page + row + 8) * NG + u * REP + rep) * 4);
-          const float2 sa = pair(pa[0]), sb = pair(pb[0]);
+          const float2 sa = pair(vp[b][0][u]), sb = pair(vp[b][1][u]);
           const float ma = fmaf(8.f, sa.x, sa.y), mb = fmaf(8.f, sb.x, sb.y);
           pmt.x = fmaf(p[b][0], ma, fmaf(p[b][2], mb, pmt.x));
           pmt.y = fmaf(p[b][1], ma, fmaf(p[b][3], mb, pmt.y));
           wt[b][0] = transpose8x8(f16x2(p[b][0] * sa.x, p[b][1] * sa.x));
           wt[b][1] = transpose8x8(f16x2(p[b][2] * sb.x, p[b][3] * sb.x));
         }
-        // -8 2^-24 and -8 2^-20, as the codes of these rows are held
+        // Rows `row` take whole bytes n0 + 16 n1, rows `row` + 8 the codes 16 n1 in
+        // them; n0 is the difference. Eight for n: -(8 + 128) 2^-24 and -128 2^-24.
 #pragma unroll
         for (int b = 0; b < kTile; ++b)
-          mma(off, 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, wt[b][0], wt[b][1], off);
+          mma(off, 0x80888088u, 0x80808080u, 0x80888088u, 0x80808080u, wt[b][0], wt[b][1], off);
         pm[u] = fma2(pm[u], alpha, mul2(pmt, make_float2(down, down)));
         // chunks c0 .. of each of the pass's groups; a column's own group counts
 #pragma unroll
@@ -499,26 +543,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
 #pragma unroll
               for (int c = 0; c < kPart; ++c) {
                 float(&lo)[4] = acc[y * kPart + c][0], (&hi)[4] = acc[y * kPart + c][1];
-                mma(lo, va[c] & 0x000f000fu, va[c] & 0x00f000f0u, vb[c] & 0x000f000fu,
+                mma(lo, va[c] & 0x00ff00ffu, va[c] & 0x00f000f0u, vb[c] & 0x00ff00ffu,
                     vb[c] & 0x00f000f0u, wt[b][0], wt[b][1], b ? lo : off);
-                const uint32_t a8 = va[c] >> 8, b8 = vb[c] >> 8;
-                mma(hi, a8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x000f000fu, b8 & 0x00f000f0u,
-                    wt[b][0], wt[b][1], b ? hi : off);
+                const uint32_t a8 = high_bytes(va[c]), b8 = high_bytes(vb[c]);
+                mma(hi, a8, a8 & 0x00f000f0u, b8, b8 & 0x00f000f0u, wt[b][0], wt[b][1],
+                    b ? hi : off);
               }
             }
           }
 #pragma unroll
           for (int c = 0; c < kPart; ++c)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float2 a = make_float2(acc[c][i >> 1][2 * (i & 1)], acc[c][i >> 1][2 * (i & 1) + 1]);
+            for (int i = 0; i < 2; ++i) {
+              float2 a[2];
 #pragma unroll
-              for (int y = 1; y < REP; ++y) {
-                a.x = rep == y ? acc[y][i >> 1][2 * (i & 1)] : a.x;
-                a.y = rep == y ? acc[y][i >> 1][2 * (i & 1) + 1] : a.y;
+              for (int k = 0; k < 2; ++k) {
+                a[k] = make_float2(acc[c][i][2 * k], acc[c][i][2 * k + 1]);
+#pragma unroll
+                for (int y = 1; y < REP; ++y) {
+                  a[k].x = rep == y ? acc[y][i][2 * k] : a[k].x;
+                  a[k].y = rep == y ? acc[y][i][2 * k + 1] : a[k].y;
+                }
               }
-              float2& o = O[u * CG + c0 + c][i];
-              o = fma2(a, i & 1 ? c20 : c24, mul2(o, alpha));
+              a[0] = fma2(a[1], make_float2(-1.f, -1.f), a[0]);
+              float2(&o)[4] = O[u * CG + c0 + c];
+              o[2 * i] = fma2(a[0], c24, mul2(o[2 * i], alpha));
+              o[2 * i + 1] = fma2(a[1], c20, mul2(o[2 * i + 1], alpha));
             }
         }
       }
@@ -676,59 +726,50 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
   }
 
   // ------------------------------------------------ join the CTAs' parts
-  // Those are the CTA's first segment, if it does not begin here or goes on, and
-  // its last, if it goes on.
-  const Kv4Place head = kv4_place(first, R, Hk, cb), tail = kv4_place(first, R, Hk, ce - 1);
-  const bool tail_out = tail.blk + 1 < tail.nblk;
-  const bool head_out = head.blk > 0, same = head.r == tail.r && head.h == tail.h;
-  if (!head_out && !tail_out) return;
-  __threadfence();
+  // Thread 0 announces the head part, thread 32 the tail part. The barrier
+  // orders the CTA's writes before the announcement that releases them.
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const Kv4Place seg = k ? tail : head;
-    const long long x0 = (long long)Hk * first[seg.r] + (long long)seg.h * seg.nblk;
-    const int c0 = kv4_worker(W, N, x0), c1 = kv4_worker(W, N, x0 + seg.nblk - 1);
-    if (tid == k * 32) {
-      bool last = false;
-      if (k ? tail_out && !(same && head_out) : head_out) {
-        last = atomicAdd(P.counters + c0, 1) == c1 - c0;
-        if (last) P.counters[c0] = 0;  // as the next call finds it
-        __threadfence();
-      }
-      misc[k] = last;
+    if (tid != k * 32) continue;
+    const Shared m = out[k];
+    int last = 0;
+    if (m.c1 > m.c0) {
+      int before;
+      asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+                   : "=r"(before)
+                   : "l"(P.counters + m.c0)
+                   : "memory");
+      last = before == m.c1 - m.c0;
+      if (last) P.counters[m.c0] = 0;  // as the next call finds it
     }
+    misc[k] = last;
   }
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     if (!misc[k]) continue;
-    const Kv4Place seg = k ? tail : head;
-    const long long x0 = (long long)Hk * first[seg.r] + (long long)seg.h * seg.nblk;
-    const int c0 = kv4_worker(W, N, x0), c1 = kv4_worker(W, N, x0 + seg.nblk - 1);
-    const auto part_of = [&](int c) {
-      return P.part + ((long long)c * (2 + kWarps) + (c == c0 ? 1 : 0)) * part_stride;
-    };
+    const Shared m = out[k];
     for (int i = tid; i < G * D / 4; i += kThreads) {
       const int g = i / (D / 4);
-      float mx = -INFINITY;
-#pragma unroll 4
-      for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, __ldcg(part_of(c) + G * D + 2 * g));
-      const float base = mx == -INFINITY ? 0.f : mx;
-      float sum = 0.f;
+      float mx = -INFINITY, sum = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-      for (int c = c0; c <= c1; ++c) {
-        const float2 m2 = __ldcg(reinterpret_cast<const float2*>(part_of(c) + G * D + 2 * g));
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of(c)) + i);
-        const float e = ex2(m2.x - base);
-        sum = fmaf(m2.y, e, sum);
-        acc.x = fmaf(v.x, e, acc.x);
-        acc.y = fmaf(v.y, e, acc.y);
-        acc.z = fmaf(v.z, e, acc.z);
-        acc.w = fmaf(v.w, e, acc.w);
+      for (int c = m.c0; c <= m.c1; ++c) {
+        const float* part =
+            P.part + ((long long)c * (2 + kWarps) + (c == m.c0 ? 1 : 0)) * part_stride;
+        const float2 m2 = __ldcg(reinterpret_cast<const float2*>(part + G * D + 2 * g));
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(part) + i);
+        const float top = fmaxf(mx, m2.x), base = top == -INFINITY ? 0.f : top;
+        const float e0 = ex2(mx - base), e = ex2(m2.x - base);
+        mx = top;
+        sum = fmaf(m2.y, e, sum * e0);
+        acc.x = fmaf(v.x, e, acc.x * e0);
+        acc.y = fmaf(v.y, e, acc.y * e0);
+        acc.z = fmaf(v.z, e, acc.z * e0);
+        acc.w = fmaf(v.w, e, acc.w * e0);
       }
-      const long long orow = (long long)seg.r * P.H + (long long)seg.h * G + g;
+      const long long orow = (long long)m.r * P.H + (long long)m.h * G + g;
       const float inv = 1.f / sum;
       uint2 v;
       v.x = float_to_row2<FP16>(acc.x * inv, acc.y * inv);

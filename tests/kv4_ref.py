@@ -89,12 +89,13 @@ def attend_bounds(o, lse, parts, dtype):
     Each weight p s is rounded once to fp16 (half a step: 2^-11 of it), which moves O by at most
     2^-11 E[s |n - 8|]. A score carries the fp32 roundings of d products and sums (below 2^-17 of
     sum |q_i k_i| for d <= 128, 128 roundings of 2^-24 each) and moves O by twice that times
-    E|v - o|, LSE by once. The fp32 products and sums over the keys (of codes up to 16 s, then of
-    the parts) add below 2^-16 of E[16 s] + |o|: a hundred roundings of 2^-23 and as much again.
+    E|v - o|, LSE by once. The fp32 products and sums over the keys are of bytes, two codes each:
+    of up to 256 s, in parts of 64 keys. A part's five additions, each off by 2^-23 of that, add
+    5 2^-23 16 < 2^-16 of E[16 s], the joining of the parts as much again of E[16 s] + |o|.
     The output is rounded once."""
     spread, wide, dev, big = parts
     score = big.unsqueeze(-1) * 2.0 ** -17
-    bound = 2.0 ** -11 * spread + 2 * score * dev + 2.0 ** -16 * (wide + o.abs())
+    bound = 2.0 ** -11 * spread + 2 * score * dev + 2.0 ** -15 * (wide + o.abs())
     bound = bound + EPS[dtype] / 2 * (o.abs() + bound) + 2.0 ** -24
     return bound, big * 2.0 ** -17 + 2.0 ** -20 * (1 + lse.abs().nan_to_num(0, 0, 0))
 
