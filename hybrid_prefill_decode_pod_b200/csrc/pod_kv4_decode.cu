@@ -39,10 +39,11 @@
 namespace pod {
 namespace {
 
-constexpr int kWarps = 12;
+constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 4;   // blocks of 16 tokens between two rescales
-constexpr int kSlots = 6;  // blocks in a warp's ring
+constexpr int kSlots = 8;  // blocks in a warp's ring
+constexpr int kKeys = 4;   // blocks whose scores are taken together
 constexpr int kMaxG = 8;
 constexpr int kLeast = 16;  // blocks that make another CTA worth its join
 constexpr float kLn2 = 0.69314718055994531f;
@@ -404,42 +405,45 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
       // ---- scores of the tile's tokens: rows `row`, `row` + 8 of each block
       float p[kTile][4];
       {
-        uint32_t ka[kTile][NC], kb[kTile][NC], kp[kTile][2][NP];
 #pragma unroll
-        for (int b = 0; b < kTile; ++b) {
-          own_pairs<NP, REP>(kp[b][0], at[b] + 16 * D + (row * NG + rep) * 4);
-          own_pairs<NP, REP>(kp[b][1], at[b] + 16 * D + ((row + 8) * NG + rep) * 4);
-          lds<NC>(ka[b], at[b] + lane * (D / 8));
-          lds<NC>(kb[b], at[b] + 4 * D + lane * (D / 8));
-        }
+        for (int h = 0; h < kTile; h += kKeys) {
+          uint32_t ka[kKeys][NC], kb[kKeys][NC], kp[kKeys][2][NP];
 #pragma unroll
-        for (int u = 0; u < NP; ++u) {
-          float acc[kTile][4];
-#pragma unroll
-          for (int b = 0; b < kTile; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[b][i] = 0.f;
-#pragma unroll
-          for (int c = u * REP * CG; c < (u + 1) * REP * CG; ++c) {
-#pragma unroll
-            for (int b = 0; b < kTile; ++b)
-              mma(acc[b], ka[b][c] & 0x000f000fu, kb[b][c] & 0x000f000fu, ka[b][c] & 0x00f000f0u,
-                  kb[b][c] & 0x00f000f0u, qf[c][0], qf[c][1], acc[b]);
-#pragma unroll
-            for (int b = 0; b < kTile; ++b) {
-              const uint32_t a8 = ka[b][c] >> 8, b8 = kb[b][c] >> 8;
-              mma(acc[b], a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x00f000f0u,
-                  qf[c][2], qf[c][3], acc[b]);
-            }
+          for (int b = 0; b < kKeys; ++b) {
+            own_pairs<NP, REP>(kp[b][0], at[h + b] + 16 * D + (row * NG + rep) * 4);
+            own_pairs<NP, REP>(kp[b][1], at[h + b] + 16 * D + ((row + 8) * NG + rep) * 4);
+            lds<NC>(ka[b], at[h + b] + lane * (D / 8));
+            lds<NC>(kb[b], at[h + b] + 4 * D + lane * (D / 8));
           }
 #pragma unroll
-          for (int b = 0; b < kTile; ++b) {
-            const float2 sa = pair(kp[b][0][u]), sb = pair(kp[b][1][u]);
+          for (int u = 0; u < NP; ++u) {
+            float acc[kKeys][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 sm = i < 2 ? sa : sb;
-              const float mq = u ? fmaf(sm.y, qs[u][i & 1], p[b][i]) : sm.y * qs[u][i & 1];
-              p[b][i] = fmaf(sm.x, acc[b][i], mq);
+            for (int b = 0; b < kKeys; ++b)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[b][i] = 0.f;
+#pragma unroll
+            for (int c = u * REP * CG; c < (u + 1) * REP * CG; ++c) {
+#pragma unroll
+              for (int b = 0; b < kKeys; ++b)
+                mma(acc[b], ka[b][c] & 0x000f000fu, kb[b][c] & 0x000f000fu, ka[b][c] & 0x00f000f0u,
+                    kb[b][c] & 0x00f000f0u, qf[c][0], qf[c][1], acc[b]);
+#pragma unroll
+              for (int b = 0; b < kKeys; ++b) {
+                const uint32_t a8 = ka[b][c] >> 8, b8 = kb[b][c] >> 8;
+                mma(acc[b], a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x00f000f0u,
+                    qf[c][2], qf[c][3], acc[b]);
+              }
+            }
+#pragma unroll
+            for (int b = 0; b < kKeys; ++b) {
+              const float2 sa = pair(kp[b][0][u]), sb = pair(kp[b][1][u]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 sm = i < 2 ? sa : sb;
+                const float mq = u ? fmaf(sm.y, qs[u][i & 1], p[h + b][i]) : sm.y * qs[u][i & 1];
+                p[h + b][i] = fmaf(sm.x, acc[b][i], mq);
+              }
             }
           }
         }
