@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <climits>
 #include <cstdint>
 
 #include "pod_kv4_params.h"
@@ -48,28 +49,21 @@ __device__ __forceinline__ int pair_byte(int kv, int token, int grp, int ngrp) {
   return kKv4Page * D + ((kv * kKv4Page + token) * ngrp + grp) * 4;
 }
 
-// The request of row i: the largest r with cu[r] <= i, or -1 if cu leaves the
-// row out. cu is read within its num_reqs + 1 entries whatever it holds.
-__device__ __forceinline__ int row_request(const int* __restrict__ cu, int n, int i) {
-  int lo = 0, hi = n;  // cu[lo] <= i < cu[hi] if the row belongs to any
+// The largest r < n with cu[r] <= i (0 if there is none), by the whole warp: each
+// round divides the range by 33. cu is read within its n + 1 entries whatever
+// it holds.
+__device__ __forceinline__ int warp_request(const int* __restrict__ cu, int n, int i, int lane) {
+  int lo = 0, hi = n;
   while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(cu + mid) <= i)
-      lo = mid;
-    else
-      hi = mid;
+    const int probe = lo + (int)((long long)(hi - lo) * (lane + 1) / 33);
+    const uint32_t below = __ballot_sync(0xffffffffu, __ldg(cu + probe) <= i);
+    // the probes that are not above i, counted from the first: cu is sorted
+    const int k = below == 0xffffffffu ? 32 : __ffs(~below) - 1;
+    const int next_lo = lo + (int)((long long)(hi - lo) * k / 33);
+    hi = k == 32 ? hi : max(lo + (int)((long long)(hi - lo) * (k + 1) / 33), next_lo + 1);
+    lo = next_lo;
   }
-  return __ldg(cu + lo) <= i && i < __ldg(cu + lo + 1) ? lo : -1;
-}
-
-// The record of (request r, position pos, KV head h), or nullptr where the
-// position is outside the table row or the page outside the pool.
-__device__ __forceinline__ unsigned char* record_of(const Kv4Rows& P, int r, long long pos, int h,
-                                                    int rec_bytes) {
-  if (pos < 0 || (pos >> 4) >= P.table_stride) return nullptr;
-  const int page = __ldg(P.table + (long long)r * P.table_stride + (pos >> 4));
-  if (page < 0 || page >= P.pool_blocks) return nullptr;
-  return P.pool + ((long long)page * P.Hk + h) * rec_bytes;
+  return lo;
 }
 
 }  // namespace pod

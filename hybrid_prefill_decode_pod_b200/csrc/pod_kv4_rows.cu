@@ -2,243 +2,411 @@
 // norm with rotation, quantising rows into the cache, and reading them back.
 // All three are bound by memory: a lane handles eight adjacent channels of one
 // head's row (16 bytes), D / 8 lanes share a row.
+#include <algorithm>
+
 #include "pod_kv4.cuh"
 
 namespace pod {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 
-template <int D>
-__device__ __forceinline__ float row_sum(float x) {
-#pragma unroll
-  for (int o = D / 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-
-// y = x / sqrt(mean(x^2) + eps) * w, then the rotation, rounded once. The lane
-// that holds a channel's partner (rot / 2 channels away) sends its unrounded
-// values by shuffle.
-template <int D, bool FP16, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const QkParams P) {
-  constexpr int kLanes = D / 8;
-  const int lane = threadIdx.x & 31, l = lane % kLanes;
-  const int heads = P.heads[0] + P.heads[1];
-  const long long total = (long long)P.num_rows * heads;
-  const long long item0 = ((long long)blockIdx.x * kThreads + threadIdx.x) / kLanes;
-  const bool in_range = item0 < total;
-  const long long item = in_range ? item0 : total - 1;
-  const int row = (int)(item / heads), hh = (int)(item % heads);
-  const int side = hh >= P.heads[0], h = side ? hh - P.heads[0] : hh;
-  const int pos = __ldg(P.positions + row);
-  const bool live = in_range && pos >= 0;
-
-  uint4 raw = make_uint4(0, 0, 0, 0);
-  if (live)
-    raw = *reinterpret_cast<const uint4*>(P.in[side] + row * P.in_row[side] + h * P.in_head[side] +
-                                          8 * l);
-  float x[8];
-  const uint32_t rw[4] = {raw.x, raw.y, raw.z, raw.w};
+template <bool FP16>
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = row2_to_float<FP16>(rw[i]);
+    const float2 f = row2_to_float<FP16>(w[i]);
     x[2 * i] = f.x;
     x[2 * i + 1] = f.y;
   }
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-  ss = row_sum<D>(ss);
-  if (P.weight[side]) {
-    const float inv = 1.0f / sqrtf(ss * (1.0f / D) + P.eps);
-    const uint4 wv = __ldg(reinterpret_cast<const uint4*>(P.weight[side] + 8 * l));
-    const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = row2_to_float<FP16>(ww[i]);
-      x[2 * i] = x[2 * i] * inv * f.x;
-      x[2 * i + 1] = x[2 * i + 1] * inv * f.y;
-    }
-  }
+}
+template <bool FP16>
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(float_to_row2<FP16>(x[0], x[1]), float_to_row2<FP16>(x[2], x[3]),
+                    float_to_row2<FP16>(x[4], x[5]), float_to_row2<FP16>(x[6], x[7]));
+}
+
+// y = x / sqrt(mean(x^2) + eps) * w, then the rotation, rounded once.
+//
+// A warp takes some heads of one row, 256 / D of them at a time (kBatch loads in
+// flight). The angle's cosines and sines belong to the row, so a lane multiplies
+// them with its weights once, y_i = inv (x_i a_i + x_partner b_i), and a head
+// costs two multiply-adds for each channel. The partner, rot / 2 channels away,
+// comes by shuffle as it was read.
+constexpr int kBatch = 4;
+
+template <int D, bool FP16, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const QkParams P, int parts) {
+  constexpr int kLanes = D / 8, kHeads = 32 / kLanes;
+  const int lane = threadIdx.x & 31, l = lane % kLanes, sub = lane / kLanes;
+  const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int row = unit / parts, part = unit % parts;
+  if (row >= P.num_rows) return;
+  const int pos = __ldg(P.positions + row);
+  if (pos < 0) return;
   const int half = P.rot / 2;
-  const bool rotated = 8 * l < P.rot;
-  const bool angle = pos < P.max_position;
-  const float* cs = P.cos_sin + (long long)(live && angle ? pos : 0) * P.rot;
-  if constexpr (INTERLEAVED) {
-    if (rotated && live && angle) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(cs + 4 * l));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(cs + half + 4 * l));
-      const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+  const bool rotated = 8 * l < P.rot, first = 8 * l < half;
+  const int partner = INTERLEAVED || !rotated ? lane : first ? lane + half / 8 : lane - half / 8;
+  float cs[8], sn[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = a * cc[i] - b * sn[i];
-        x[2 * i + 1] = a * sn[i] + b * cc[i];
+  for (int i = 0; i < 8; ++i) {
+    cs[i] = 1.f;
+    sn[i] = 0.f;
+  }
+  if (pos >= P.max_position) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cs[i] = __int_as_float(0x7fffffff);
+  } else if (rotated) {
+    const float* t = P.cos_sin + (long long)pos * P.rot;
+    if constexpr (INTERLEAVED) {
+      const float4 c = __ldg(reinterpret_cast<const float4*>(t + 4 * l));
+      const float4 s = __ldg(reinterpret_cast<const float4*>(t + half + 4 * l));
+      const float c4[4] = {c.x, c.y, c.z, c.w}, s4[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        cs[i] = c4[i / 2];
+        sn[i] = i & 1 ? s4[i / 2] : -s4[i / 2];
       }
-    }
-  } else {
-    const bool first = 8 * l < half;
-    const int partner = rotated ? (first ? lane + half / 8 : lane - half / 8) : lane;
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], partner);
-    if (rotated && live && angle) {
+    } else {
       const int at = first ? 8 * l : 8 * l - half;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const float4 c = __ldg(reinterpret_cast<const float4*>(cs + at + 4 * q));
-        const float4 s = __ldg(reinterpret_cast<const float4*>(cs + half + at + 4 * q));
-        const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+        const float4 c = __ldg(reinterpret_cast<const float4*>(t + at + 4 * q));
+        const float4 s = __ldg(reinterpret_cast<const float4*>(t + half + at + 4 * q));
+        const float c4[4] = {c.x, c.y, c.z, c.w}, s4[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int k = 4 * q + i;
-          x[k] = x[k] * cc[i] + (first ? -y[k] : y[k]) * sn[i];
+          cs[4 * q + i] = c4[i];
+          sn[4 * q + i] = first ? -s4[i] : s4[i];
         }
       }
     }
   }
-  if (!live) return;
-  if (!angle) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __int_as_float(0x7fffffff);
+  for (int side = 0; side < 2; ++side) {
+    const int n = P.heads[side];
+    const int each = (n + parts * kHeads - 1) / (parts * kHeads) * kHeads;
+    const int h0 = part * each, h1 = min(n, h0 + each);
+    if (h0 >= h1) continue;
+    const bool norm = P.weight[side] != nullptr;
+    float a[8], b[8];
+    if (norm) {
+      float w[8], wp[8];
+      unpack8<FP16>(__ldg(reinterpret_cast<const uint4*>(P.weight[side] + 8 * l)), w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        wp[i] = INTERLEAVED ? w[i ^ 1] : __shfl_sync(0xffffffffu, w[i], partner);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        a[i] = w[i] * cs[i];
+        b[i] = wp[i] * sn[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        a[i] = cs[i];
+        b[i] = sn[i];
+      }
+    }
+    const uint16_t* in = P.in[side] + row * P.in_row[side] + 8 * l;
+    uint16_t* out = P.out[side] + row * P.out_row[side] + 8 * l;
+    for (int h = h0; h < h1; h += kHeads * kBatch) {
+      uint4 raw[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        raw[k] = make_uint4(0, 0, 0, 0);
+        const int hh = h + k * kHeads + sub;
+        if (hh < h1) raw[k] = *reinterpret_cast<const uint4*>(in + hh * P.in_head[side]);
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int hh = h + k * kHeads + sub;
+        float x[8], y[8];
+        unpack8<FP16>(raw[k], x);
+        float inv = 1.f;
+        if (norm) {
+          float ss = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+          for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          inv = rsqrtf(fmaf(ss, 1.0f / D, P.eps));
+        }
+        if constexpr (INTERLEAVED) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
+        } else {
+          uint4 p;
+          p.x = __shfl_sync(0xffffffffu, raw[k].x, partner);
+          p.y = __shfl_sync(0xffffffffu, raw[k].y, partner);
+          p.z = __shfl_sync(0xffffffffu, raw[k].z, partner);
+          p.w = __shfl_sync(0xffffffffu, raw[k].w, partner);
+          unpack8<FP16>(p, y);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float z = x[i] * a[i];
+          x[i] = (rotated ? fmaf(y[i], b[i], z) : z) * inv;
+        }
+        if (hh < h1) *reinterpret_cast<uint4*>(out + hh * P.out_head[side]) = pack8<FP16>(x);
+      }
+    }
   }
-  uint4 out;
-  out.x = float_to_row2<FP16>(x[0], x[1]);
-  out.y = float_to_row2<FP16>(x[2], x[3]);
-  out.z = float_to_row2<FP16>(x[4], x[5]);
-  out.w = float_to_row2<FP16>(x[6], x[7]);
-  *reinterpret_cast<uint4*>(P.out[side] + row * P.out_row[side] + h * P.out_head[side] + 8 * l) = out;
 }
 
-// A row's token and head: item = (row, K or V, head).
-struct Place {
-  int row, kv, h;
-  bool live;  // the row belongs to a request
-  long long pos;
-  unsigned char* rec;
+// ------------------------------------------------------------ cache rows
+//
+// A CTA looks at 16 adjacent rows. Those at which a page begins (or a request's
+// first row) stand for the rows of that page that follow, and a warp takes one
+// such page of one KV head: up to 16 tokens and one record.
+
+// Row `lane` of the CTA's 16 rows (lanes 0 .. 15).
+struct Row {
+  int count;           // tokens of its page from here on, 0 where it begins none
+  int token;           // its token within the page
+  const int* page;     // its table entry, or nullptr outside the table
 };
 
-template <int D>
-__device__ __forceinline__ Place place_of(const Kv4Rows& P, int rec_bytes) {
-  const int per_row = 2 * P.Hk;
-  const long long total = (long long)P.num_rows * per_row;
-  const long long item0 = ((long long)blockIdx.x * kThreads + threadIdx.x) / (D / 8);
-  const long long item = item0 < total ? item0 : total - 1;
-  Place p;
-  p.row = (int)(item / per_row);
-  const int sub = (int)(item % per_row);
-  p.kv = sub >= P.Hk;
-  p.h = p.kv ? sub - P.Hk : sub;
-  const int r = row_request(P.cu_rows, P.num_reqs, p.row);
-  p.live = item0 < total && r >= 0;
-  p.pos = r >= 0 ? (long long)__ldg(P.start + r) + p.row - __ldg(P.cu_rows + r) : -1;
-  p.rec = r >= 0 ? record_of(P, r, p.pos, p.h, rec_bytes) : nullptr;
-  return p;
+__device__ __forceinline__ Row row_of(const Kv4Rows& P, int row0, int lane) {
+  Row out{0, 0, nullptr};
+  const int row = row0 + lane;
+  // requests of the 16 rows: the first one's, and how many begin behind it
+  const int r0 = warp_request(P.cu_rows, P.num_reqs, row0, lane);
+  const int next = r0 + 1 + lane <= P.num_reqs ? __ldg(P.cu_rows + r0 + 1 + lane) : INT_MAX;
+  int r = r0;
+  if (__shfl_sync(0xffffffffu, next, 31) > row0 + 15) {
+    int more = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int n = __popc(__ballot_sync(0xffffffffu, next <= row0 + i));
+      if (lane == i) more = n;
+    }
+    r = r0 + more;
+  } else {  // more than 31 requests end here (empty ones among them)
+    int hi = P.num_reqs;
+    while (hi - r > 1) {
+      const int mid = (r + hi) >> 1;
+      if (__ldg(P.cu_rows + mid) <= row)
+        r = mid;
+      else
+        hi = mid;
+    }
+  }
+  if (lane < 16 && row < P.num_rows && r < P.num_reqs) {
+    const int begin = __ldg(P.cu_rows + r), end = min(__ldg(P.cu_rows + r + 1), P.num_rows);
+    if (begin <= row && row < end) {
+      const long long pos = (long long)__ldg(P.start + r) + row - begin;
+      out.token = (int)(pos & 15);
+      if (row == begin || row == 0 || out.token == 0) out.count = min(16 - out.token, end - row);
+      if (pos >= 0 && (pos >> 4) < P.table_stride)
+        out.page = P.table + (long long)r * P.table_stride + (pos >> 4);
+    }
+  }
+  return out;
 }
 
+// Calls f(first row, tokens, first token, page id or -1, head) for each page and
+// head of the CTA's rows, one warp each.
+template <typename F>
+__device__ __forceinline__ void for_pages(const Kv4Rows& P, F f) {
+  const int lane = threadIdx.x & 31, row0 = blockIdx.x * 16;
+  const Row mine = row_of(P, row0, lane);
+  int page = -1;
+  if (mine.count && mine.page) {
+    page = __ldg(mine.page);
+    if (page >= P.pool_blocks) page = -1;
+  }
+  const uint32_t begins = __ballot_sync(0xffffffffu, mine.count > 0);
+  const int rank = mine.count > 0 ? __popc(begins & ((1u << lane) - 1)) : -1;
+  const int heads = (P.Hk + gridDim.y - 1) / gridDim.y, h0 = blockIdx.y * heads;
+  const int nh = min(heads, P.Hk - h0), units = __popc(begins) * nh;
+  for (int u = threadIdx.x >> 5; u < units; u += kWarps) {
+    const int i = __ffs(__ballot_sync(0xffffffffu, rank == u / nh)) - 1;
+    f(row0 + i, __shfl_sync(0xffffffffu, mine.count, i), __shfl_sync(0xffffffffu, mine.token, i),
+      __shfl_sync(0xffffffffu, page, i), h0 + u % nh);
+  }
+}
+
+// s and m of a group from its least and largest value (as the header states).
+__device__ __forceinline__ __half2 pair_of(float lo, float hi, bool fine) {
+  const __half2 sm = __halves2half2(__float2half_rn((hi - lo) / 15.0f), __float2half_rn(lo));
+  const uint32_t nan = 0x7fff7fffu;
+  return fine ? sm : *reinterpret_cast<const __half2*>(&nan);
+}
+
+// Codes of eight values. (x - m) / s is first taken with the reciprocal, which is
+// off by less than 2^-22 of 16; where that could change the code, the exact
+// quotient decides.
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float s, float m) {
+  if (!(s > 0.f)) return 0;
+  const float inv = 1.0f / s;
+  uint32_t code = 0;
+  float worst = 0.f;
+#pragma unroll
+  for (int i = 7; i >= 0; --i) {
+    const float t = fminf(fmaxf((x[i] - m) * inv, 0.f), 15.f);
+    const float n = t + 12582912.f;  // the nearest integer in the low bits
+    worst = fmaxf(worst, fabsf(t - (n - 12582912.f)));
+    code = code << 4 | (__float_as_uint(n) & 15u);
+  }
+  if (worst > 0.49999f) {
+    code = 0;
+#pragma unroll
+    for (int i = 7; i >= 0; --i)
+      code = code << 4 | (uint32_t)rintf(fminf(fmaxf((x[i] - m) / s, 0.f), 15.f));
+  }
+  return code;
+}
+
+// Bound by the rows' bytes, D bytes of codes for 4 D of K and V. A whole page is
+// put together in shared memory, since V's codes of a token lie 16 bytes apart,
+// and leaves in 16-byte pieces; part of a page goes to its places directly.
 template <int D, int GROUP, bool FP16>
 __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4Rows P) {
-  constexpr int kLanes = D / 8, NG = D / GROUP;
-  const int l = (threadIdx.x & 31) % kLanes;
-  const Place p = place_of<D>(P, kv4_record_bytes(D, GROUP));
-  const bool live = p.live && p.rec != nullptr;
-  uint4 raw = make_uint4(0, 0, 0, 0);
-  if (live)
-    raw = *reinterpret_cast<const uint4*>(P.x[p.kv] + p.row * P.row[p.kv] + p.h * P.head[p.kv] +
-                                          8 * l);
-  const uint32_t rw[4] = {raw.x, raw.y, raw.z, raw.w};
-  float x[8], lo = 65504.f, hi = -65504.f;
-  bool fine = true;
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, NG = D / GROUP;
+  constexpr int kRec = kv4_record_bytes(D, GROUP);
+  constexpr int kFlight = 8;  // loads in flight
+  __shared__ __align__(16) unsigned char stage[kWarps][kRec];
+  const int lane = threadIdx.x & 31, l = lane % kLanes, sub = lane / kLanes;
+  unsigned char* mine = stage[threadIdx.x >> 5];
+  for_pages(P, [&](int row, int count, int token, int page, int h) {
+    if (page < 0) return;
+    unsigned char* rec = P.pool + ((long long)page * P.Hk + h) * kRec;
+    const bool whole = count == 16;
+    unsigned char* to = whole ? mine : rec;
+    const uint16_t* ks = P.x[0] + row * P.row[0] + h * P.head[0] + 8 * l;
+    const uint16_t* vs = P.x[1] + row * P.row[1] + h * P.head[1] + 8 * l;
+    // the tokens' rows of K, then those of V
+    for (int q0 = 0; q0 < 2 * count; q0 += kRows * kFlight) {
+      uint4 raw[kFlight];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = row2_to_float<FP16>(rw[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
+      for (int k = 0; k < kFlight; ++k) {
+        const int q = q0 + k * kRows + sub;
+        raw[k] = make_uint4(0, 0, 0, 0);
+        if (q < 2 * count)
+          raw[k] = *reinterpret_cast<const uint4*>(q < count ? ks + q * P.row[0]
+                                                             : vs + (q - count) * P.row[1]);
+      }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    fine = fine && fabsf(x[i]) < __int_as_float(0x7f800000);
-    x[i] = fminf(fmaxf(x[i], -65504.f), 65504.f);
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-  }
-  int ok = fine;
+      for (int k = 0; k < kFlight; ++k) {
+        if (q0 + k * kRows >= 2 * count) break;
+        const int q = q0 + k * kRows + sub, kv = q >= count, t = token + (kv ? q - count : q);
+        float x[8], lo = 65504.f, hi = -65504.f, size = 0.f;
+        unpack8<FP16>(raw[k], x);
 #pragma unroll
-  for (int o = GROUP / 16; o; o >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    ok &= __shfl_xor_sync(0xffffffffu, ok, o);
-  }
-  if (!live) return;
-  const __half sh = ok ? __float2half_rn((hi - lo) / 15.0f) : __ushort_as_half(0x7fff);
-  const __half mh = ok ? __float2half_rn(lo) : __ushort_as_half(0x7fff);
-  const float s = __half2float(sh), m = __half2float(mh);
-  uint32_t code = 0;
-  if (s > 0.f) {
+        for (int i = 0; i < 8; ++i) {
+          size = fmaf(x[i], 0.f, size);  // NaN where a value is not finite
+          if (!FP16) x[i] = fminf(fmaxf(x[i], -65504.f), 65504.f);
+          lo = fminf(lo, x[i]);
+          hi = fmaxf(hi, x[i]);
+        }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      code |= (uint32_t)fminf(fmaxf(rintf((x[i] - m) / s), 0.f), 15.f) << (4 * i);
-  }
-  const int t = (int)(p.pos & 15);
-  if (p.kv == 0) {
-    *reinterpret_cast<uint32_t*>(p.rec + k_code_byte<D>(t, l)) = code;
-  } else {
-    *reinterpret_cast<uint16_t*>(p.rec + v_code_byte<D>(t, 2 * l)) = (uint16_t)code;
-    *reinterpret_cast<uint16_t*>(p.rec + v_code_byte<D>(t, 2 * l + 1)) = (uint16_t)(code >> 16);
-  }
-  if (8 * l % GROUP == 0)
-    *reinterpret_cast<__half2*>(p.rec + pair_byte<D>(p.kv, t, 8 * l / GROUP, NG)) =
-        __halves2half2(sh, mh);
+        for (int o = GROUP / 16; o; o >>= 1) {
+          lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+          hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+          size += __shfl_xor_sync(0xffffffffu, size, o);
+        }
+        if (q >= 2 * count) continue;
+        const __half2 sm = pair_of(lo, hi, size == 0.f);
+        const uint32_t code = codes_of(x, __low2float(sm), __high2float(sm));
+        if (kv == 0) {
+          *reinterpret_cast<uint32_t*>(to + k_code_byte<D>(t, l)) = code;
+        } else {
+          *reinterpret_cast<uint16_t*>(to + v_code_byte<D>(t, 2 * l)) = (uint16_t)code;
+          *reinterpret_cast<uint16_t*>(to + v_code_byte<D>(t, 2 * l + 1)) = (uint16_t)(code >> 16);
+        }
+        if (8 * l % GROUP == 0)
+          *reinterpret_cast<__half2*>(to + pair_byte<D>(kv, t, 8 * l / GROUP, NG)) = sm;
+      }
+    }
+    if (whole) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < (kRec + 511) / 512; ++i)
+        if (i * 512 + lane * 16 < kRec)
+          *reinterpret_cast<uint4*>(rec + i * 512 + lane * 16) =
+              *reinterpret_cast<const uint4*>(mine + i * 512 + lane * 16);
+      __syncwarp();
+    }
+  });
 }
 
+// The reverse: the record comes to shared memory in 16-byte pieces, the rows
+// leave in 16 bytes a lane.
 template <int D, int GROUP, bool FP16>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Rows P) {
-  constexpr int kLanes = D / 8, NG = D / GROUP;
-  const int l = (threadIdx.x & 31) % kLanes;
-  const Place p = place_of<D>(P, kv4_record_bytes(D, GROUP));
-  if (!p.live) return;
-  float s = __int_as_float(0x7fffffff), m = s;
-  uint32_t code = 0;
-  if (p.rec) {
-    const int t = (int)(p.pos & 15);
-    if (p.kv == 0)
-      code = *reinterpret_cast<const uint32_t*>(p.rec + k_code_byte<D>(t, l));
-    else
-      code = *reinterpret_cast<const uint16_t*>(p.rec + v_code_byte<D>(t, 2 * l)) |
-             (uint32_t)*reinterpret_cast<const uint16_t*>(p.rec + v_code_byte<D>(t, 2 * l + 1)) << 16;
-    const __half2 sm =
-        *reinterpret_cast<const __half2*>(p.rec + pair_byte<D>(p.kv, t, 8 * l / GROUP, NG));
-    s = __low2float(sm);
-    m = __high2float(sm);
-  }
-  float x[8];
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, NG = D / GROUP;
+  constexpr int kRec = kv4_record_bytes(D, GROUP);
+  __shared__ __align__(16) unsigned char stage[kWarps][kRec];
+  const int lane = threadIdx.x & 31, l = lane % kLanes, sub = lane / kLanes;
+  unsigned char* mine = stage[threadIdx.x >> 5];
+  for_pages(P, [&](int row, int count, int token, int page, int h) {
+    if (page >= 0) {
+      const unsigned char* rec = P.pool + ((long long)page * P.Hk + h) * kRec;
+      uint4 v[(kRec + 511) / 512];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = fmaf((float)(code >> (4 * i) & 15), s, m);
-  uint4 out;
-  out.x = float_to_row2<FP16>(x[0], x[1]);
-  out.y = float_to_row2<FP16>(x[2], x[3]);
-  out.z = float_to_row2<FP16>(x[4], x[5]);
-  out.w = float_to_row2<FP16>(x[6], x[7]);
-  *reinterpret_cast<uint4*>(P.x[p.kv] + p.row * P.row[p.kv] + p.h * P.head[p.kv] + 8 * l) = out;
-}
-
-unsigned blocks_for(long long items, int D) {
-  return (unsigned)((items * (D / 8) + kThreads - 1) / kThreads);
+      for (int i = 0; i < (kRec + 511) / 512; ++i)
+        if (i * 512 + lane * 16 < kRec)
+          v[i] = __ldg(reinterpret_cast<const uint4*>(rec + i * 512 + lane * 16));
+#pragma unroll
+      for (int i = 0; i < (kRec + 511) / 512; ++i)
+        if (i * 512 + lane * 16 < kRec)
+          *reinterpret_cast<uint4*>(mine + i * 512 + lane * 16) = v[i];
+    }
+    __syncwarp();
+    uint16_t* kd = P.x[0] + row * P.row[0] + h * P.head[0] + 8 * l;
+    uint16_t* vd = P.x[1] + row * P.row[1] + h * P.head[1] + 8 * l;
+#pragma unroll 4
+    for (int q = sub; q < 2 * count; q += kRows) {
+      const int kv = q >= count, i = kv ? q - count : q, t = token + i;
+      float s = __int_as_float(0x7fffffff), m = s;
+      uint32_t code = 0;
+      if (page >= 0) {
+        if (kv == 0)
+          code = *reinterpret_cast<const uint32_t*>(mine + k_code_byte<D>(t, l));
+        else
+          code = *reinterpret_cast<const uint16_t*>(mine + v_code_byte<D>(t, 2 * l)) |
+                 (uint32_t)*reinterpret_cast<const uint16_t*>(mine + v_code_byte<D>(t, 2 * l + 1))
+                     << 16;
+        const __half2 sm =
+            *reinterpret_cast<const __half2*>(mine + pair_byte<D>(kv, t, 8 * l / GROUP, NG));
+        s = __low2float(sm);
+        m = __high2float(sm);
+      }
+      float x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)  // 2^23 + n, less 2^23: an exact conversion
+        x[k] = fmaf(__uint_as_float((code >> (4 * k) & 15u) | 0x4b000000u) - 8388608.f, s, m);
+      *reinterpret_cast<uint4*>(kv ? vd + i * P.row[1] : kd + i * P.row[0]) = pack8<FP16>(x);
+    }
+    __syncwarp();
+  });
 }
 
 template <int D, bool FP16>
 cudaError_t norm_rope_of(const QkParams& P, int interleaved, cudaStream_t s) {
-  const unsigned grid = blocks_for((long long)P.num_rows * (P.heads[0] + P.heads[1]), D);
+  // Few rows are cut into parts of one batch of heads at least.
+  constexpr int kHeads = 256 / D;
+  const int most = std::max(P.heads[0], P.heads[1]);
+  const long long want = 148 * 4 * kWarps;
+  long long parts = std::min<long long>((want + P.num_rows - 1) / P.num_rows,
+                                        (most + kHeads - 1) / kHeads);
+  parts = std::max<long long>(parts, 1);
+  const unsigned grid = (unsigned)((P.num_rows * parts + kWarps - 1) / kWarps);
   if (interleaved)
-    norm_rope_kernel<D, FP16, true><<<grid, kThreads, 0, s>>>(P);
+    norm_rope_kernel<D, FP16, true><<<grid, kThreads, 0, s>>>(P, (int)parts);
   else
-    norm_rope_kernel<D, FP16, false><<<grid, kThreads, 0, s>>>(P);
+    norm_rope_kernel<D, FP16, false><<<grid, kThreads, 0, s>>>(P, (int)parts);
   return cudaGetLastError();
 }
 
 template <int D, int GROUP>
 cudaError_t rows_of(const Kv4Rows& P, int dtype, bool read, cudaStream_t s) {
-  const unsigned grid = blocks_for((long long)P.num_rows * 2 * P.Hk, D);
+  // With few rows every KV head has CTAs of its own.
+  const unsigned windows = (unsigned)((P.num_rows + 15) / 16);
+  const dim3 grid(windows, windows >= 2 * 148 ? (P.Hk + kWarps - 1) / kWarps : P.Hk);
   if (read) {
     if (dtype)
       kv4_read_kernel<D, GROUP, true><<<grid, kThreads, 0, s>>>(P);
