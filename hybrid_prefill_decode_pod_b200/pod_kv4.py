@@ -13,6 +13,7 @@ into a CUDA graph and replayed with what its tensors hold then. As in
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional
 
 import torch
@@ -20,6 +21,7 @@ import torch
 from .pod_attn import POD_OK, PodError, load_library
 
 PAGE_SIZE = 16
+_I32, _U8, _F32 = torch.int32, torch.uint8, torch.float32
 DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
 # Every symbol include/pod_kv4.h declares.
@@ -58,6 +60,33 @@ class QkArgs(ctypes.Structure):
                 ("max_position", _ll)]
 
 
+# The C structs are filled with struct.pack, in one call: setting the fields of a
+# ctypes.Structure one by one takes longer than the launch.
+_CODES = {_i: "i", _ll: "q", _vp: "P", ctypes.c_float: "f"}
+
+
+def _packer(cls) -> struct.Struct:
+    fmt = "".join(_CODES[t] for _, t in cls._fields_)
+    n = struct.calcsize(fmt)
+    packer = struct.Struct(fmt + "%dx" % (ctypes.sizeof(cls) - n))
+    assert packer.size == ctypes.sizeof(cls)
+    return packer
+
+
+_pack_rows = _packer(Kv4RowsArgs).pack
+_pack_decode = _packer(Kv4DecodeArgs).pack
+_pack_qk = _packer(QkArgs).pack
+
+
+class Args:
+    """The C struct of one call, and the tensors it points into."""
+
+    __slots__ = ("struct", "device", "keep")
+
+    def __init__(self, packed: bytes, device: int, keep: tuple):
+        self.struct, self.device, self.keep = packed, device, keep
+
+
 _bound = None
 
 
@@ -65,12 +94,12 @@ def _library() -> ctypes.CDLL:
     global _bound
     if _bound is None:
         lib = load_library()
-        lib.pod_qk_norm_rope.argtypes = [ctypes.POINTER(QkArgs), _vp]
+        lib.pod_qk_norm_rope.argtypes = [_vp, _vp]
         lib.pod_kv4_record_bytes.argtypes = [_i, _i]
         lib.pod_kv4_create.argtypes = [ctypes.POINTER(_vp), ctypes.POINTER(Kv4Config)]
-        lib.pod_kv4_write.argtypes = [_vp, ctypes.POINTER(Kv4RowsArgs), _vp]
-        lib.pod_kv4_read.argtypes = [_vp, ctypes.POINTER(Kv4RowsArgs), _vp]
-        lib.pod_kv4_decode.argtypes = [_vp, ctypes.POINTER(Kv4DecodeArgs), _vp]
+        lib.pod_kv4_write.argtypes = [_vp, _vp, _vp]
+        lib.pod_kv4_read.argtypes = [_vp, _vp, _vp]
+        lib.pod_kv4_decode.argtypes = [_vp, _vp, _vp]
         lib.pod_kv4_destroy.argtypes = [_vp]
         for name in EXPORTED:
             getattr(lib, name).restype = ctypes.c_int
@@ -83,22 +112,21 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _on(t: torch.Tensor, device: int, dtype, name: str) -> int:
-    """The pointer of a CUDA tensor of the given device and type."""
-    if not (t.is_cuda and t.get_device() == device and t.dtype == dtype):
-        raise ValueError("%s: expected a %s CUDA tensor on device %d" % (name, dtype, device))
-    return t.data_ptr()
+def _refuse(device: int, tensors) -> None:
+    """Says which (name, tensor, dtype) is no CUDA tensor of that type on that device, or not
+    contiguous (a name that ends in "=" need not be)."""
+    for name, t, dtype in tensors:
+        if t.dtype is not dtype or t.get_device() != device or device < 0:
+            raise ValueError("%s: expected a %s CUDA tensor on device %d"
+                             % (name.rstrip("="), dtype, device))
+        if name[-1] != "=" and not t.is_contiguous():
+            raise ValueError("%s: expected a contiguous tensor" % name)
 
 
-def _flat(t: torch.Tensor, device: int, dtype, name: str) -> int:
-    """The pointer of a contiguous one."""
-    if not t.is_contiguous():
-        raise ValueError("%s: expected a contiguous tensor" % name)
-    return _on(t, device, dtype, name)
-
-
-def _stream_of(stream, device: int) -> int:
-    return int((torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
+def _raw_stream(stream, device: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return int(stream.cuda_stream)
 
 
 def record_bytes(head_dim: int, group_size: int) -> int:
@@ -124,77 +152,96 @@ class PodKv4:
         rc = self._lib.pod_kv4_create(ctypes.byref(h), ctypes.byref(self.cfg))
         if rc != POD_OK:
             raise PodError(rc, "pod_kv4_create")
-        self._h = h
+        self._h = h.value
         self.dtype = dtype
         self.device = int(device)
         self.record = record_bytes(head_dim, group_size)
+        self._per_page = (int(num_kv_heads), self.record)
+        self._kv = (int(num_kv_heads), int(head_dim))
+        self._qo = (int(num_qo_heads), int(head_dim))
 
     def new_pool(self, pool_blocks: int) -> torch.Tensor:
         """A zeroed pool (every code and pair stands for 0)."""
         return torch.zeros(pool_blocks, self.cfg.num_kv_heads, self.record, dtype=torch.uint8,
                            device="cuda:%d" % self.device)
 
-    # -- argument structs (each keeps its tensors alive)
-    def _cache(self, a, pool, block_table, num_reqs) -> None:
-        _need(pool.dim() == 3 and tuple(pool.shape[1:]) == (self.cfg.num_kv_heads, self.record),
-              "pool: expected [blocks, num_kv_heads, %d]" % self.record)
-        _need(block_table.dim() == 2 and block_table.shape[0] == num_reqs,
-              "block_table: expected [num_reqs, pages]")
-        a.num_reqs = num_reqs
-        a.pool = _flat(pool, self.device, torch.uint8, "pool")
-        a.pool_blocks = pool.shape[0]
-        a.block_table = _flat(block_table, self.device, torch.int32, "block_table")
-        a.block_table_stride = block_table.shape[1]
+    # -- arguments (each keeps its tensors alive)
+    def _cache(self, pool, block_table, num_reqs):
+        """(blocks in the pool, pages in a row of the table)"""
+        ps, ts = pool.shape, block_table.shape
+        if ps[1:] != self._per_page:
+            raise ValueError("pool: expected [blocks, num_kv_heads, %d]" % self.record)
+        if len(ts) != 2 or ts[0] != num_reqs:
+            raise ValueError("block_table: expected [num_reqs, pages]")
+        return ps[0], ts[1]
 
-    def rows_args(self, cu_rows, start, k, v, pool, block_table) -> Kv4RowsArgs:
+    def rows_args(self, cu_rows, start, k, v, pool, block_table) -> Args:
         """``k``, ``v``: [rows, Hk, d], any row and head strides that are multiples of 8."""
-        a = Kv4RowsArgs()
-        n = start.numel()
-        _need(cu_rows.numel() == n + 1, "cu_rows: expected num_reqs + 1 entries")
-        self._cache(a, pool, block_table, n)
-        shape = k.shape
-        _need(len(shape) == 3 and shape == v.shape and
-              tuple(shape[1:]) == (self.cfg.num_kv_heads, self.cfg.head_dim),
-              "k, v: expected [rows, num_kv_heads, head_dim]")
-        ks, vs = k.stride(), v.stride()
-        _need(ks[2] == 1 and vs[2] == 1, "k, v: expected adjacent channels")
-        a.num_rows = shape[0]
-        a.cu_rows = _flat(cu_rows, self.device, torch.int32, "cu_rows")
-        a.start = _flat(start, self.device, torch.int32, "start")
-        a.k, a.v = _on(k, self.device, self.dtype, "k"), _on(v, self.device, self.dtype, "v")
-        a.k_row_stride, a.k_head_stride, a.v_row_stride, a.v_head_stride = ks[0], ks[1], vs[0], vs[1]
-        a._keep = (cu_rows, start, k, v, pool, block_table)
-        return a
+        dev, dtype = self.device, self.dtype
+        if not (k.dtype is dtype and v.dtype is dtype and cu_rows.dtype is _I32
+                and start.dtype is _I32 and pool.dtype is _U8 and block_table.dtype is _I32
+                and k.get_device() == dev and v.get_device() == dev
+                and cu_rows.get_device() == dev and start.get_device() == dev
+                and pool.get_device() == dev and block_table.get_device() == dev
+                and cu_rows.is_contiguous() and start.is_contiguous()
+                and pool.is_contiguous() and block_table.is_contiguous()):
+            _refuse(dev, (("cu_rows", cu_rows, _I32), ("start", start, _I32), ("k=", k, dtype),
+                          ("v=", v, dtype), ("pool", pool, _U8), ("block_table", block_table, _I32)))
+        n, shape, ks, vs = start.numel(), k.shape, k.stride(), v.stride()
+        blocks, pages = self._cache(pool, block_table, n)
+        if cu_rows.numel() != n + 1:
+            raise ValueError("cu_rows: expected num_reqs + 1 entries")
+        if len(shape) != 3 or shape != v.shape or shape[1:] != self._kv:
+            raise ValueError("k, v: expected [rows, num_kv_heads, head_dim]")
+        if ks[2] != 1 or vs[2] != 1:
+            raise ValueError("k, v: expected adjacent channels")
+        return Args(_pack_rows(n, shape[0], cu_rows.data_ptr(), start.data_ptr(), k.data_ptr(),
+                               v.data_ptr(), ks[0], ks[1], vs[0], vs[1], pool.data_ptr(), blocks,
+                               block_table.data_ptr(), pages),
+                    dev, (cu_rows, start, k, v, pool, block_table))
 
-    def decode_args(self, ctx_lens, q, o, lse, pool, block_table) -> Kv4DecodeArgs:
-        a = Kv4DecodeArgs()
-        n = ctx_lens.numel()
-        H, d = self.cfg.num_qo_heads, self.cfg.head_dim
-        _need(q.shape == (n, H, d) and o.shape == (n, H, d),
-              "q, o: expected [num_reqs, num_qo_heads, head_dim]")
-        _need(lse.shape == (n, H), "lse: expected [num_reqs, num_qo_heads]")
-        self._cache(a, pool, block_table, n)
-        a.ctx_lens = _flat(ctx_lens, self.device, torch.int32, "ctx_lens")
-        a.q, a.o = _flat(q, self.device, self.dtype, "q"), _flat(o, self.device, self.dtype, "o")
-        a.lse = _flat(lse, self.device, torch.float32, "lse")
-        a._keep = (ctx_lens, q, o, lse, pool, block_table)
-        return a
+    def decode_args(self, ctx_lens, q, o, lse, pool, block_table) -> Args:
+        dev, dtype = self.device, self.dtype
+        if not (q.dtype is dtype and o.dtype is dtype and lse.dtype is _F32
+                and ctx_lens.dtype is _I32 and pool.dtype is _U8 and block_table.dtype is _I32
+                and q.get_device() == dev and o.get_device() == dev and lse.get_device() == dev
+                and ctx_lens.get_device() == dev and pool.get_device() == dev
+                and block_table.get_device() == dev
+                and q.is_contiguous() and o.is_contiguous() and lse.is_contiguous()
+                and ctx_lens.is_contiguous() and pool.is_contiguous()
+                and block_table.is_contiguous()):
+            _refuse(dev, (("ctx_lens", ctx_lens, _I32), ("q", q, dtype), ("o", o, dtype),
+                          ("lse", lse, _F32), ("pool", pool, _U8), ("block_table", block_table, _I32)))
+        n, shape = ctx_lens.numel(), q.shape
+        blocks, pages = self._cache(pool, block_table, n)
+        if shape != (n, *self._qo) or o.shape != shape:
+            raise ValueError("q, o: expected [num_reqs, num_qo_heads, head_dim]")
+        if lse.shape != shape[:2]:
+            raise ValueError("lse: expected [num_reqs, num_qo_heads]")
+        return Args(_pack_decode(n, ctx_lens.data_ptr(), q.data_ptr(), o.data_ptr(),
+                                 lse.data_ptr(), pool.data_ptr(), blocks, block_table.data_ptr(),
+                                 pages),
+                    dev, (ctx_lens, q, o, lse, pool, block_table))
 
     # -- calls
-    def _call(self, name, args, stream) -> None:
-        _need(self._h is not None, "the context is closed")
-        rc = getattr(self._lib, name)(self._h, ctypes.byref(args), _stream_of(stream, self.device))
+    def write(self, args: Args, stream=None) -> None:
+        rc = self._lib.pod_kv4_write(self._h, args.struct, _raw_stream(stream, self.device))
         if rc != POD_OK:
-            raise PodError(rc, name)
+            self._failed(rc, "pod_kv4_write")
 
-    def write(self, args: Kv4RowsArgs, stream=None) -> None:
-        self._call("pod_kv4_write", args, stream)
+    def read(self, args: Args, stream=None) -> None:
+        rc = self._lib.pod_kv4_read(self._h, args.struct, _raw_stream(stream, self.device))
+        if rc != POD_OK:
+            self._failed(rc, "pod_kv4_read")
 
-    def read(self, args: Kv4RowsArgs, stream=None) -> None:
-        self._call("pod_kv4_read", args, stream)
+    def decode(self, args: Args, stream=None) -> None:
+        rc = self._lib.pod_kv4_decode(self._h, args.struct, _raw_stream(stream, self.device))
+        if rc != POD_OK:
+            self._failed(rc, "pod_kv4_decode")
 
-    def decode(self, args: Kv4DecodeArgs, stream=None) -> None:
-        self._call("pod_kv4_decode", args, stream)
+    def _failed(self, rc: int, name: str) -> None:
+        _need(self._h is not None, "the context is closed")
+        raise PodError(rc, name)
 
     def close(self) -> int:
         if getattr(self, "_h", None):
@@ -222,52 +269,67 @@ def rope_table(max_position: int, rot_dim: int, base: float = 10000.0, *,
     return torch.cat([angle.cos(), angle.sin()], 1).float()
 
 
+_NOTHING = (0, 0, 0, 0, 0, 0, 0)  # a side that is left out
+
+
+def _side(name, x, out, weight, rows, d, dtype, device):
+    """(heads, rows, output, the four strides) of q or k, and its weight."""
+    if out is None:
+        out = x
+    if not (x.dtype is dtype and out.dtype is dtype and device >= 0
+            and x.get_device() == device and out.get_device() == device):
+        _refuse(device, ((name + "=", x, dtype), (name + "_out=", out, dtype)))
+    shape, xs, os = x.shape, x.stride(), out.stride()
+    if len(shape) != 3 or shape[0] != rows or shape[2] != d or out.shape != shape:
+        raise ValueError("%s: expected [rows, heads, head_dim], and its output alike" % name)
+    if xs[2] != 1 or os[2] != 1:
+        raise ValueError("%s: expected adjacent channels" % name)
+    w = 0
+    if weight is not None:
+        if weight.dtype is not dtype or weight.get_device() != device or not weight.is_contiguous():
+            _refuse(device, ((name + "_weight", weight, dtype),))
+        if weight.shape != (d,):
+            raise ValueError("%s_weight: expected [head_dim]" % name)
+        w = weight.data_ptr()
+    return (shape[1], x.data_ptr(), out.data_ptr(), xs[0], xs[1], os[0], os[1]), w
+
+
 def norm_rope_args(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.Tensor,
                    cos_sin: torch.Tensor, *, q_out: Optional[torch.Tensor] = None,
                    k_out: Optional[torch.Tensor] = None,
                    q_weight: Optional[torch.Tensor] = None,
                    k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
-                   interleaved: bool = False) -> QkArgs:
+                   interleaved: bool = False) -> Args:
     """``q`` [rows, H, d] and ``k`` [rows, Hk, d] (either may be None), with any
     row and head strides that are multiples of 8. Without ``q_out`` / ``k_out``
     the rows are replaced in place; without a weight that side is only rotated."""
-    a = QkArgs()
     some = q if q is not None else k
-    _need(some is not None, "q or k is needed")
-    device, dtype, rows, d = some.get_device(), some.dtype, some.shape[0], some.shape[-1]
-    _need(dtype in DTYPES, "q, k: bfloat16 or float16")
-    for name, x, out, w in (("q", q, q_out, q_weight), ("k", k, k_out, k_weight)):
-        if x is None:
-            continue
-        out = x if out is None else out
-        _need(x.dim() == 3 and x.shape[0] == rows and x.shape[2] == d and out.shape == x.shape,
-              "%s: expected [rows, heads, head_dim], and its output alike" % name)
-        xs, os = x.stride(), out.stride()
-        _need(xs[2] == 1 and os[2] == 1, "%s: expected adjacent channels" % name)
-        setattr(a, name, _on(x, device, dtype, name))
-        setattr(a, name + "_out", _on(out, device, dtype, name + "_out"))
-        setattr(a, name + "_row_stride", xs[0])
-        setattr(a, name + "_head_stride", xs[1])
-        setattr(a, name + "_out_row_stride", os[0])
-        setattr(a, name + "_out_head_stride", os[1])
-        if w is not None:
-            _need(w.shape == (d,), "%s_weight: expected [head_dim]" % name)
-            setattr(a, name + "_weight", _flat(w, device, dtype, name + "_weight"))
-    a.num_qo_heads = 0 if q is None else q.shape[1]
-    a.num_kv_heads = 0 if k is None else k.shape[1]
-    _need(positions.shape == (rows,), "positions: expected [rows]")
-    _need(cos_sin.dim() == 2, "cos_sin: expected [max_position, rot_dim]")
-    a.head_dim, a.rot_dim, a.num_rows = d, cos_sin.shape[1], rows
-    a.interleaved, a.dtype, a.device, a.eps = int(interleaved), DTYPES[dtype], device, eps
-    a.positions = _flat(positions, device, torch.int32, "positions")
-    a.cos_sin = _flat(cos_sin, device, torch.float32, "cos_sin")
-    a.max_position = cos_sin.shape[0]
-    a._keep = (q, k, positions, cos_sin, q_out, k_out, q_weight, k_weight)
-    return a
+    if some is None:
+        raise ValueError("q or k is needed")
+    device, dtype, size = some.get_device(), some.dtype, some.shape
+    rows, d = size[0], size[-1]
+    if dtype not in DTYPES:
+        raise ValueError("q, k: bfloat16 or float16")
+    qs, qw = (_NOTHING, 0) if q is None else _side("q", q, q_out, q_weight, rows, d, dtype, device)
+    ks, kw = (_NOTHING, 0) if k is None else _side("k", k, k_out, k_weight, rows, d, dtype, device)
+    if not (positions.dtype is _I32 and cos_sin.dtype is _F32
+            and positions.get_device() == device and cos_sin.get_device() == device
+            and positions.is_contiguous() and cos_sin.is_contiguous()):
+        _refuse(device, (("positions", positions, _I32), ("cos_sin", cos_sin, _F32)))
+    angles = cos_sin.shape
+    if positions.shape != (rows,):
+        raise ValueError("positions: expected [rows]")
+    if len(angles) != 2:
+        raise ValueError("cos_sin: expected [max_position, rot_dim]")
+    far, rot = angles
+    return Args(_pack_qk(qs[0], ks[0], d, rot, 1 if interleaved else 0, DTYPES[dtype], device, rows,
+                         qs[1], ks[1], qs[2], ks[2], qs[3], qs[4], ks[3], ks[4], qs[5], qs[6],
+                         ks[5], ks[6], qw, kw, eps, positions.data_ptr(), cos_sin.data_ptr(), far),
+                device, (q, k, positions, cos_sin, q_out, k_out, q_weight, k_weight))
 
 
-def qk_norm_rope(args: QkArgs, stream=None) -> None:
+def qk_norm_rope(args: Args, stream=None) -> None:
     """``pod_qk_norm_rope``: per-head RMS norm of q and k and the rotation, in one launch."""
-    rc = _library().pod_qk_norm_rope(ctypes.byref(args), _stream_of(stream, args.device))
+    rc = _library().pod_qk_norm_rope(args.struct, _raw_stream(stream, args.device))
     if rc != POD_OK:
         raise PodError(rc, "pod_qk_norm_rope")

@@ -224,6 +224,14 @@ def test_rope_table_is_exact_far_out():
         assert abs(t[pos, i].item() - math.cos(a)) < 1e-7 and abs(t[pos, 32 + i].item() - math.sin(a)) < 1e-7
 
 
+def test_packed_structs_are_the_c_structs():
+    """What the binding packs is what the ctypes mirror of the header's struct reads."""
+    for cls, pack in ((p4.Kv4RowsArgs, p4._pack_rows), (p4.Kv4DecodeArgs, p4._pack_decode), (p4.QkArgs, p4._pack_qk)):
+        values = [float(i) + 0.5 if t is ctypes.c_float else 1000 + i for i, (_, t) in enumerate(cls._fields_)]
+        got = cls.from_buffer_copy(pack(*values))
+        assert [getattr(got, name) for name, _ in cls._fields_] == values
+
+
 def test_binding_refuses_tensors_of_the_host():
     x = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
