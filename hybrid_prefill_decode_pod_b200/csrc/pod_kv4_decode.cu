@@ -57,23 +57,6 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
         "f"(c[3]));
 }
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{.reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
-      "fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{.reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
-      "mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -117,10 +100,6 @@ __device__ bool slow_wait(uint32_t bar, uint32_t parity) {
 }
 // The upper bytes of both halves
 __device__ __forceinline__ uint32_t high_bytes(uint32_t v) { return __byte_perm(v, 0, 0x4341); }
-__device__ __forceinline__ float2 pair(uint32_t v) {
-  return __half22float2(*reinterpret_cast<__half2*>(&v));
-}
-
 // max or sum over the eight rows of a fragment (lanes 4 apart)
 __device__ __forceinline__ float rows_max(float x) {
 #pragma unroll

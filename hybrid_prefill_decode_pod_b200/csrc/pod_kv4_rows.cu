@@ -38,7 +38,7 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 constexpr int kBatch = 4;
 
 template <int D, bool FP16, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const QkParams P, int parts) {
+__global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const QkParams P, int parts) {
   constexpr int kLanes = D / 8, kHeads = 32 / kLanes;
   const int lane = threadIdx.x & 31, l = lane % kLanes, sub = lane / kLanes;
   const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -49,41 +49,6 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const QkParams P, i
   const int half = P.rot / 2;
   const bool rotated = 8 * l < P.rot, first = 8 * l < half;
   const int partner = INTERLEAVED || !rotated ? lane : first ? lane + half / 8 : lane - half / 8;
-  float cs[8], sn[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    cs[i] = 1.f;
-    sn[i] = 0.f;
-  }
-  if (pos >= P.max_position) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = __int_as_float(0x7fffffff);
-  } else if (rotated) {
-    const float* t = P.cos_sin + (long long)pos * P.rot;
-    if constexpr (INTERLEAVED) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(t + 4 * l));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(t + half + 4 * l));
-      const float c4[4] = {c.x, c.y, c.z, c.w}, s4[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        cs[i] = c4[i / 2];
-        sn[i] = i & 1 ? s4[i / 2] : -s4[i / 2];
-      }
-    } else {
-      const int at = first ? 8 * l : 8 * l - half;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const float4 c = __ldg(reinterpret_cast<const float4*>(t + at + 4 * q));
-        const float4 s = __ldg(reinterpret_cast<const float4*>(t + half + at + 4 * q));
-        const float c4[4] = {c.x, c.y, c.z, c.w}, s4[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          cs[4 * q + i] = c4[i];
-          sn[4 * q + i] = first ? -s4[i] : s4[i];
-        }
-      }
-    }
-  }
 #pragma unroll
   for (int side = 0; side < 2; ++side) {
     const int n = P.heads[side];
@@ -91,6 +56,41 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const QkParams P, i
     const int h0 = part * each, h1 = min(n, h0 + each);
     if (h0 >= h1) continue;
     const bool norm = P.weight[side] != nullptr;
+    float cs[8], sn[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      cs[i] = 1.f;
+      sn[i] = 0.f;
+    }
+    if (pos >= P.max_position) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) cs[i] = __int_as_float(0x7fffffff);
+    } else if (rotated) {
+      const float* t = P.cos_sin + (long long)pos * P.rot;
+      if constexpr (INTERLEAVED) {
+        const float4 c = __ldg(reinterpret_cast<const float4*>(t + 4 * l));
+        const float4 s = __ldg(reinterpret_cast<const float4*>(t + half + 4 * l));
+        const float c4[4] = {c.x, c.y, c.z, c.w}, s4[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          cs[i] = c4[i / 2];
+          sn[i] = i & 1 ? s4[i / 2] : -s4[i / 2];
+        }
+      } else {
+        const int at = first ? 8 * l : 8 * l - half;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float4 c = __ldg(reinterpret_cast<const float4*>(t + at + 4 * q));
+          const float4 s = __ldg(reinterpret_cast<const float4*>(t + half + at + 4 * q));
+          const float c4[4] = {c.x, c.y, c.z, c.w}, s4[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            cs[4 * q + i] = c4[i];
+            sn[4 * q + i] = first ? -s4[i] : s4[i];
+          }
+        }
+      }
+    }
     float a[8], b[8];
     if (norm) {
       float w[8], wp[8];
@@ -229,45 +229,110 @@ __device__ __forceinline__ void for_pages(const Kv4Rows& P, F f) {
   }
 }
 
-// s and m of a group from its least and largest value (as the header states).
-__device__ __forceinline__ __half2 pair_of(float lo, float hi, bool fine) {
-  const __half2 sm = __halves2half2(__float2half_rn((hi - lo) / 15.0f), __float2half_rn(lo));
-  const uint32_t nan = 0x7fff7fffu;
-  return fine ? sm : *reinterpret_cast<const __half2*>(&nan);
+// Least (NaN if either is) of two values each.
+template <bool FP16>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  if constexpr (FP16) {
+    const __half2 r = __hmin2_nan(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<__nv_bfloat162*>(&a),
+                                         *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
 }
 
-// Codes of eight values. (x - m) / s is first taken with the reciprocal, which is
-// off by less than 2^-22 of 16; where that could change the code, the exact
-// quotient decides.
-__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float s, float m) {
-  if (!(s > 0.f)) return 0;
-  const float inv = 1.0f / s;
-  uint32_t code = 0;
-  float worst = 0.f;
+// Codes of a lane's eight values, and the pair of their group, which GROUP / 8
+// adjacent lanes share (all lanes of the warp call this).
+//
+// The least and the largest value are taken in the row's own type, two at a
+// time: low halves hold least values, high halves the negated largest. A NaN or
+// an infinity shows in them. The quotient is first taken with an approximate
+// reciprocal, off by less than 2^-18 of a code; where that could change a code,
+// or a value lies outside the codes (fp16(lo) may be above lo, and values are
+// cut to fp16's range), the quotient itself decides.
+struct Quantised {
+  uint32_t code;
+  __half2 pair;
+};
+
+template <int GROUP, bool FP16>
+__device__ __forceinline__ Quantised quantise(const uint4& raw) {
+  constexpr uint32_t kNeg = 0x80008000u;
+  const uint32_t least = min2<FP16>(min2<FP16>(raw.x, raw.y), min2<FP16>(raw.z, raw.w));
+  const uint32_t most = min2<FP16>(min2<FP16>(raw.x ^ kNeg, raw.y ^ kNeg),
+                                   min2<FP16>(raw.z ^ kNeg, raw.w ^ kNeg));
+  uint32_t ends = min2<FP16>(__byte_perm(least, most, 0x5410), __byte_perm(least, most, 0x7632));
 #pragma unroll
-  for (int i = 7; i >= 0; --i) {
-    const float t = fminf(fmaxf((x[i] - m) * inv, 0.f), 15.f);
-    const float n = t + 12582912.f;  // the nearest integer in the low bits
-    worst = fmaxf(worst, fabsf(t - (n - 12582912.f)));
-    code = code << 4 | (__float_as_uint(n) & 15u);
+  for (int o = GROUP / 16; o; o >>= 1)
+    ends = min2<FP16>(ends, __shfl_xor_sync(0xffffffffu, ends, o));
+  float2 e = row2_to_float<FP16>(ends);
+  const bool fine = fabsf(e.x) < INFINITY && fabsf(e.y) < INFINITY;
+  float lo = e.x, hi = -e.y;
+  if (!FP16) {
+    lo = fminf(fmaxf(lo, -65504.f), 65504.f);
+    hi = fminf(fmaxf(hi, -65504.f), 65504.f);
   }
-  if (worst > 0.49999f) {
+  Quantised q;
+  const uint32_t nan = 0x7fff7fffu;
+  q.pair = fine ? __halves2half2(__float2half_rn((hi - lo) / 15.0f), __float2half_rn(lo))
+                : *reinterpret_cast<const __half2*>(&nan);
+  const float s = __low2float(q.pair), m = __high2float(q.pair);
+  q.code = 0;
+  if (!(s > 0.f)) return q;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  const float2 inv2 = make_float2(inv, inv), m2 = make_float2(-m, -m);
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  float worst = fmaxf((m - e.x) * inv, (-e.y - m) * inv - 15.f);
+  uint32_t code = 0;
+#pragma unroll
+  for (int i = 3; i >= 0; --i) {
+    const float2 t = mul2(add2(row2_to_float<FP16>(w[i]), m2), inv2);
+    const float2 n = add2(t, make_float2(12582912.f, 12582912.f));  // the integer in the low bits
+    const float2 d = add2(add2(n, make_float2(-12582912.f, -12582912.f)), make_float2(-t.x, -t.y));
+    worst = fmaxf(worst, fmaxf(fabsf(d.x), fabsf(d.y)));
+    code = (code << 4) + __float_as_uint(n.y);
+    code = (code << 4) + __float_as_uint(n.x);
+  }
+  q.code = code - 0x3f400000u;  // the other bits of the eight 12582912 + n
+  if (worst > 0.4999f) {
     code = 0;
 #pragma unroll
-    for (int i = 7; i >= 0; --i)
-      code = code << 4 | (uint32_t)rintf(fminf(fmaxf((x[i] - m) / s, 0.f), 15.f));
+    for (int i = 3; i >= 0; --i) {
+      const float2 x = row2_to_float<FP16>(w[i]);
+      code = code << 4 | (uint32_t)rintf(fminf(fmaxf((x.y - m) / s, 0.f), 15.f));
+      code = code << 4 | (uint32_t)rintf(fminf(fmaxf((x.x - m) / s, 0.f), 15.f));
+    }
+    q.code = code;
   }
-  return code;
+  return q;
+}
+
+// The eight values of a word of codes. A code in the low bits of an fp16 is the
+// subnormal n 2^-24 (n 2^-20 one code higher), and s 2^24 is exact.
+template <bool FP16>
+__device__ __forceinline__ uint4 values(uint32_t code, uint32_t sm) {
+  const float2 p = pair(sm);
+  const float2 s24 = make_float2(p.x * 0x1p24f, p.x * 0x1p24f);
+  const float2 s20 = make_float2(p.x * 0x1p20f, p.x * 0x1p20f), m = make_float2(p.y, p.y);
+  const uint32_t up = code >> 8;
+  const float2 a = fma2(pair(code & 0x000f000fu), s24, m);  // channels 0 and 4
+  const float2 b = fma2(pair(code & 0x00f000f0u), s20, m);
+  const float2 c = fma2(pair(up & 0x000f000fu), s24, m);
+  const float2 d = fma2(pair(up & 0x00f000f0u), s20, m);
+  return make_uint4(float_to_row2<FP16>(a.x, b.x), float_to_row2<FP16>(c.x, d.x),
+                    float_to_row2<FP16>(a.y, b.y), float_to_row2<FP16>(c.y, d.y));
 }
 
 // Bound by the rows' bytes, D bytes of codes for 4 D of K and V. A whole page is
 // put together in shared memory, since V's codes of a token lie 16 bytes apart,
 // and leaves in 16-byte pieces; part of a page goes to its places directly.
 template <int D, int GROUP, bool FP16>
-__global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4Rows P) {
+__global__ void __launch_bounds__(kThreads, 4) kv4_write_kernel(const Kv4Rows P) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, NG = D / GROUP;
   constexpr int kRec = kv4_record_bytes(D, GROUP);
-  constexpr int kFlight = 8;  // loads in flight
+  constexpr int kFlight = 4;  // rows of K and of V in flight
   __shared__ __align__(16) unsigned char stage[kWarps][kRec];
   const int lane = threadIdx.x & 31, l = lane % kLanes, sub = lane / kLanes;
   unsigned char* mine = stage[threadIdx.x >> 5];
@@ -276,49 +341,33 @@ __global__ void __launch_bounds__(kThreads) kv4_write_kernel(const Kv4Rows P) {
     unsigned char* rec = P.pool + ((long long)page * P.Hk + h) * kRec;
     const bool whole = count == 16;
     unsigned char* to = whole ? mine : rec;
-    const uint16_t* ks = P.x[0] + row * P.row[0] + h * P.head[0] + 8 * l;
-    const uint16_t* vs = P.x[1] + row * P.row[1] + h * P.head[1] + 8 * l;
-    // the tokens' rows of K, then those of V
-    for (int q0 = 0; q0 < 2 * count; q0 += kRows * kFlight) {
-      uint4 raw[kFlight];
+    const uint16_t* ks = P.x[0] + (row + sub) * P.row[0] + h * P.head[0] + 8 * l;
+    const uint16_t* vs = P.x[1] + (row + sub) * P.row[1] + h * P.head[1] + 8 * l;
+    for (int i0 = 0; i0 < count; i0 += kRows * kFlight) {
+      uint4 kr[kFlight], vr[kFlight];
 #pragma unroll
       for (int k = 0; k < kFlight; ++k) {
-        const int q = q0 + k * kRows + sub;
-        raw[k] = make_uint4(0, 0, 0, 0);
-        if (q < 2 * count)
-          raw[k] = *reinterpret_cast<const uint4*>(q < count ? ks + q * P.row[0]
-                                                             : vs + (q - count) * P.row[1]);
+        const int i = i0 + k * kRows;
+        kr[k] = vr[k] = make_uint4(0, 0, 0, 0);
+        if (i + sub < count) {
+          kr[k] = *reinterpret_cast<const uint4*>(ks + i * P.row[0]);
+          vr[k] = *reinterpret_cast<const uint4*>(vs + i * P.row[1]);
+        }
       }
 #pragma unroll
       for (int k = 0; k < kFlight; ++k) {
-        if (q0 + k * kRows >= 2 * count) break;
-        const int q = q0 + k * kRows + sub, kv = q >= count, t = token + (kv ? q - count : q);
-        float x[8], lo = 65504.f, hi = -65504.f, size = 0.f;
-        unpack8<FP16>(raw[k], x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          size = fmaf(x[i], 0.f, size);  // NaN where a value is not finite
-          if (!FP16) x[i] = fminf(fmaxf(x[i], -65504.f), 65504.f);
-          lo = fminf(lo, x[i]);
-          hi = fmaxf(hi, x[i]);
+        const int i = i0 + k * kRows;
+        if (i >= count) break;
+        const Quantised kq = quantise<GROUP, FP16>(kr[k]), vq = quantise<GROUP, FP16>(vr[k]);
+        if (i + sub >= count) continue;
+        const int t = token + i + sub;
+        *reinterpret_cast<uint32_t*>(to + k_code_byte<D>(t, l)) = kq.code;
+        *reinterpret_cast<uint16_t*>(to + v_code_byte<D>(t, 2 * l)) = (uint16_t)vq.code;
+        *reinterpret_cast<uint16_t*>(to + v_code_byte<D>(t, 2 * l + 1)) = (uint16_t)(vq.code >> 16);
+        if (8 * l % GROUP == 0) {
+          *reinterpret_cast<__half2*>(to + pair_byte<D>(0, t, 8 * l / GROUP, NG)) = kq.pair;
+          *reinterpret_cast<__half2*>(to + pair_byte<D>(1, t, 8 * l / GROUP, NG)) = vq.pair;
         }
-#pragma unroll
-        for (int o = GROUP / 16; o; o >>= 1) {
-          lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-          hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-          size += __shfl_xor_sync(0xffffffffu, size, o);
-        }
-        if (q >= 2 * count) continue;
-        const __half2 sm = pair_of(lo, hi, size == 0.f);
-        const uint32_t code = codes_of(x, __low2float(sm), __high2float(sm));
-        if (kv == 0) {
-          *reinterpret_cast<uint32_t*>(to + k_code_byte<D>(t, l)) = code;
-        } else {
-          *reinterpret_cast<uint16_t*>(to + v_code_byte<D>(t, 2 * l)) = (uint16_t)code;
-          *reinterpret_cast<uint16_t*>(to + v_code_byte<D>(t, 2 * l + 1)) = (uint16_t)(code >> 16);
-        }
-        if (8 * l % GROUP == 0)
-          *reinterpret_cast<__half2*>(to + pair_byte<D>(kv, t, 8 * l / GROUP, NG)) = sm;
       }
     }
     if (whole) {
@@ -356,30 +405,21 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Rows P) {
           *reinterpret_cast<uint4*>(mine + i * 512 + lane * 16) = v[i];
     }
     __syncwarp();
-    uint16_t* kd = P.x[0] + row * P.row[0] + h * P.head[0] + 8 * l;
-    uint16_t* vd = P.x[1] + row * P.row[1] + h * P.head[1] + 8 * l;
+    uint16_t* kd = P.x[0] + (row + sub) * P.row[0] + h * P.head[0] + 8 * l;
+    uint16_t* vd = P.x[1] + (row + sub) * P.row[1] + h * P.head[1] + 8 * l;
 #pragma unroll 4
-    for (int q = sub; q < 2 * count; q += kRows) {
-      const int kv = q >= count, i = kv ? q - count : q, t = token + i;
-      float s = __int_as_float(0x7fffffff), m = s;
-      uint32_t code = 0;
+    for (int i = 0; i + sub < count; i += kRows) {
+      const int t = token + i + sub;
+      uint32_t kc = 0, vc = 0, kp = 0x7fff7fffu, vp = kp;  // NaN without a place
       if (page >= 0) {
-        if (kv == 0)
-          code = *reinterpret_cast<const uint32_t*>(mine + k_code_byte<D>(t, l));
-        else
-          code = *reinterpret_cast<const uint16_t*>(mine + v_code_byte<D>(t, 2 * l)) |
-                 (uint32_t)*reinterpret_cast<const uint16_t*>(mine + v_code_byte<D>(t, 2 * l + 1))
-                     << 16;
-        const __half2 sm =
-            *reinterpret_cast<const __half2*>(mine + pair_byte<D>(kv, t, 8 * l / GROUP, NG));
-        s = __low2float(sm);
-        m = __high2float(sm);
+        kc = *reinterpret_cast<const uint32_t*>(mine + k_code_byte<D>(t, l));
+        vc = *reinterpret_cast<const uint16_t*>(mine + v_code_byte<D>(t, 2 * l)) |
+             (uint32_t)*reinterpret_cast<const uint16_t*>(mine + v_code_byte<D>(t, 2 * l + 1)) << 16;
+        kp = *reinterpret_cast<const uint32_t*>(mine + pair_byte<D>(0, t, 8 * l / GROUP, NG));
+        vp = *reinterpret_cast<const uint32_t*>(mine + pair_byte<D>(1, t, 8 * l / GROUP, NG));
       }
-      float x[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k)  // 2^23 + n, less 2^23: an exact conversion
-        x[k] = fmaf(__uint_as_float((code >> (4 * k) & 15u) | 0x4b000000u) - 8388608.f, s, m);
-      *reinterpret_cast<uint4*>(kv ? vd + i * P.row[1] : kd + i * P.row[0]) = pack8<FP16>(x);
+      *reinterpret_cast<uint4*>(kd + i * P.row[0]) = values<FP16>(kc, kp);
+      *reinterpret_cast<uint4*>(vd + i * P.row[1]) = values<FP16>(vc, vp);
     }
     __syncwarp();
   });
