@@ -8,6 +8,7 @@
 #include <cstdint>
 
 #include "pod_kv4_params.h"
+#include "pod_ptx.cuh"
 
 namespace pod {
 

@@ -229,17 +229,24 @@ __device__ __forceinline__ void for_pages(const Kv4Rows& P, F f) {
   }
 }
 
-// Least (NaN if either is) of two values each.
+// Least or largest (NaN if either is) of two values each.
 template <bool FP16>
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
-  if constexpr (FP16) {
-    const __half2 r = __hmin2_nan(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  } else {
-    const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<__nv_bfloat162*>(&a),
-                                         *reinterpret_cast<__nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
+  uint32_t r;
+  if constexpr (FP16)
+    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <bool FP16>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (FP16)
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // Codes of a lane's eight values, and the pair of their group, which GROUP / 8
@@ -248,7 +255,7 @@ __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
 // The least and the largest value are taken in the row's own type, two at a
 // time: low halves hold least values, high halves the negated largest. A NaN or
 // an infinity shows in them. The quotient is first taken with an approximate
-// reciprocal, off by less than 2^-18 of a code; where that could change a code,
+// reciprocal, off by less than 2^-17 of a code; where that could change a code,
 // or a value lies outside the codes (fp16(lo) may be above lo, and values are
 // cut to fp16's range), the quotient itself decides.
 struct Quantised {
@@ -256,30 +263,42 @@ struct Quantised {
   __half2 pair;
 };
 
+// (rarely taken: one copy for all callers)
+template <bool FP16>
+__device__ __noinline__ uint32_t exact_codes(uint4 raw, float s, float m) {
+  float x[8];
+  unpack8<FP16>(raw, x);
+  uint32_t code = 0;
+  for (int i = 0; i < 8; ++i)
+    code |= (uint32_t)rintf(fminf(fmaxf((x[i] - m) / s, 0.f), 15.f)) << (4 * i);
+  return code;
+}
+
 template <int GROUP, bool FP16>
 __device__ __forceinline__ Quantised quantise(const uint4& raw) {
-  constexpr uint32_t kNeg = 0x80008000u;
   const uint32_t least = min2<FP16>(min2<FP16>(raw.x, raw.y), min2<FP16>(raw.z, raw.w));
-  const uint32_t most = min2<FP16>(min2<FP16>(raw.x ^ kNeg, raw.y ^ kNeg),
-                                   min2<FP16>(raw.z ^ kNeg, raw.w ^ kNeg));
+  const uint32_t most =
+      max2<FP16>(max2<FP16>(raw.x, raw.y), max2<FP16>(raw.z, raw.w)) ^ 0x80008000u;
   uint32_t ends = min2<FP16>(__byte_perm(least, most, 0x5410), __byte_perm(least, most, 0x7632));
 #pragma unroll
   for (int o = GROUP / 16; o; o >>= 1)
     ends = min2<FP16>(ends, __shfl_xor_sync(0xffffffffu, ends, o));
-  float2 e = row2_to_float<FP16>(ends);
+  const float2 e = row2_to_float<FP16>(ends);
   const bool fine = fabsf(e.x) < INFINITY && fabsf(e.y) < INFINITY;
   float lo = e.x, hi = -e.y;
   if (!FP16) {
     lo = fminf(fmaxf(lo, -65504.f), 65504.f);
     hi = fminf(fmaxf(hi, -65504.f), 65504.f);
   }
+  // range / 15, rounded correctly: one residual step after the product with the
+  // rounded 1 / 15 (Markstein's method)
+  const float range = hi - lo, guess = range * (1.f / 15.f);
+  const float step = fmaf(fmaf(-guess, 15.f, range), 1.f / 15.f, guess);
   Quantised q;
   const uint32_t nan = 0x7fff7fffu;
-  q.pair = fine ? __halves2half2(__float2half_rn((hi - lo) / 15.0f), __float2half_rn(lo))
+  q.pair = fine ? __halves2half2(__float2half_rn(step), __float2half_rn(lo))
                 : *reinterpret_cast<const __half2*>(&nan);
   const float s = __low2float(q.pair), m = __high2float(q.pair);
-  q.code = 0;
-  if (!(s > 0.f)) return q;
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
   const float2 inv2 = make_float2(inv, inv), m2 = make_float2(-m, -m);
@@ -290,22 +309,17 @@ __device__ __forceinline__ Quantised quantise(const uint4& raw) {
   for (int i = 3; i >= 0; --i) {
     const float2 t = mul2(add2(row2_to_float<FP16>(w[i]), m2), inv2);
     const float2 n = add2(t, make_float2(12582912.f, 12582912.f));  // the integer in the low bits
-    const float2 d = add2(add2(n, make_float2(-12582912.f, -12582912.f)), make_float2(-t.x, -t.y));
-    worst = fmaxf(worst, fmaxf(fabsf(d.x), fabsf(d.y)));
+    const float2 d = fma2(t, make_float2(-1.f, -1.f), add2(n, make_float2(-12582912.f, -12582912.f)));
+    worst = max3(worst, fabsf(d.x), fabsf(d.y));
     code = (code << 4) + __float_as_uint(n.y);
     code = (code << 4) + __float_as_uint(n.x);
   }
-  q.code = code - 0x3f400000u;  // the other bits of the eight 12582912 + n
-  if (worst > 0.4999f) {
-    code = 0;
-#pragma unroll
-    for (int i = 3; i >= 0; --i) {
-      const float2 x = row2_to_float<FP16>(w[i]);
-      code = code << 4 | (uint32_t)rintf(fminf(fmaxf((x.y - m) / s, 0.f), 15.f));
-      code = code << 4 | (uint32_t)rintf(fminf(fmaxf((x.x - m) / s, 0.f), 15.f));
-    }
-    q.code = code;
-  }
+  code -= 0x3f400000u;  // the other bits of the eight 12582912 + n
+  q.code = code;
+  if (!(s > 0.f))
+    q.code = 0;
+  else if (worst > 0.49999f)
+    q.code = exact_codes<FP16>(raw, s, m);
   return q;
 }
 
@@ -332,7 +346,7 @@ template <int D, int GROUP, bool FP16>
 __global__ void __launch_bounds__(kThreads, 4) kv4_write_kernel(const Kv4Rows P) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, NG = D / GROUP;
   constexpr int kRec = kv4_record_bytes(D, GROUP);
-  constexpr int kFlight = 4;  // rows of K and of V in flight
+  constexpr int kFlight = 2;  // steps whose rows of K and V are in flight
   __shared__ __align__(16) unsigned char stage[kWarps][kRec];
   const int lane = threadIdx.x & 31, l = lane % kLanes, sub = lane / kLanes;
   unsigned char* mine = stage[threadIdx.x >> 5];
@@ -343,31 +357,35 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_write_kernel(const Kv4Rows P)
     unsigned char* to = whole ? mine : rec;
     const uint16_t* ks = P.x[0] + (row + sub) * P.row[0] + h * P.head[0] + 8 * l;
     const uint16_t* vs = P.x[1] + (row + sub) * P.row[1] + h * P.head[1] + 8 * l;
-    for (int i0 = 0; i0 < count; i0 += kRows * kFlight) {
-      uint4 kr[kFlight], vr[kFlight];
-#pragma unroll
-      for (int k = 0; k < kFlight; ++k) {
-        const int i = i0 + k * kRows;
-        kr[k] = vr[k] = make_uint4(0, 0, 0, 0);
-        if (i + sub < count) {
-          kr[k] = *reinterpret_cast<const uint4*>(ks + i * P.row[0]);
-          vr[k] = *reinterpret_cast<const uint4*>(vs + i * P.row[1]);
-        }
+    uint4 kr[kFlight], vr[kFlight];
+    const auto load = [&](int k, int i) {
+      if (i + sub < count) {
+        kr[k] = *reinterpret_cast<const uint4*>(ks + i * P.row[0]);
+        vr[k] = *reinterpret_cast<const uint4*>(vs + i * P.row[1]);
       }
+    };
 #pragma unroll
-      for (int k = 0; k < kFlight; ++k) {
-        const int i = i0 + k * kRows;
-        if (i >= count) break;
-        const Quantised kq = quantise<GROUP, FP16>(kr[k]), vq = quantise<GROUP, FP16>(vr[k]);
-        if (i + sub >= count) continue;
-        const int t = token + i + sub;
-        *reinterpret_cast<uint32_t*>(to + k_code_byte<D>(t, l)) = kq.code;
-        *reinterpret_cast<uint16_t*>(to + v_code_byte<D>(t, 2 * l)) = (uint16_t)vq.code;
-        *reinterpret_cast<uint16_t*>(to + v_code_byte<D>(t, 2 * l + 1)) = (uint16_t)(vq.code >> 16);
-        if (8 * l % GROUP == 0) {
-          *reinterpret_cast<__half2*>(to + pair_byte<D>(0, t, 8 * l / GROUP, NG)) = kq.pair;
-          *reinterpret_cast<__half2*>(to + pair_byte<D>(1, t, 8 * l / GROUP, NG)) = vq.pair;
-        }
+    for (int k = 0; k < kFlight; ++k) {
+      kr[k] = vr[k] = make_uint4(0, 0, 0, 0);
+      load(k, k * kRows);
+    }
+#pragma unroll 1
+    for (int i = 0; i < count; i += kRows) {
+      const Quantised kq = quantise<GROUP, FP16>(kr[0]), vq = quantise<GROUP, FP16>(vr[0]);
+#pragma unroll
+      for (int k = 0; k + 1 < kFlight; ++k) {
+        kr[k] = kr[k + 1];
+        vr[k] = vr[k + 1];
+      }
+      load(kFlight - 1, i + kFlight * kRows);
+      if (i + sub >= count) continue;
+      const int t = token + i + sub;
+      *reinterpret_cast<uint32_t*>(to + k_code_byte<D>(t, l)) = kq.code;
+      *reinterpret_cast<uint16_t*>(to + v_code_byte<D>(t, 2 * l)) = (uint16_t)vq.code;
+      *reinterpret_cast<uint16_t*>(to + v_code_byte<D>(t, 2 * l + 1)) = (uint16_t)(vq.code >> 16);
+      if (8 * l % GROUP == 0) {
+        *reinterpret_cast<__half2*>(to + pair_byte<D>(0, t, 8 * l / GROUP, NG)) = kq.pair;
+        *reinterpret_cast<__half2*>(to + pair_byte<D>(1, t, 8 * l / GROUP, NG)) = vq.pair;
       }
     }
     if (whole) {
