@@ -254,10 +254,11 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
 //
 // The least and the largest value are taken in the row's own type, two at a
 // time: low halves hold least values, high halves the negated largest. A NaN or
-// an infinity shows in them. The quotient is first taken with an approximate
-// reciprocal, off by less than 2^-17 of a code; where that could change a code,
-// or a value lies outside the codes (fp16(lo) may be above lo, and values are
-// cut to fp16's range), the quotient itself decides.
+// an infinity shows in them. Quotients often lie on the border of two codes
+// (short significands), so the product with the approximate reciprocal is
+// corrected by one residual step, which rounds it correctly. Where a value lies
+// outside the codes (fp16(lo) may be above lo, and values are cut to fp16's
+// range) the lane takes its codes once more, with limits.
 struct Quantised {
   uint32_t code;
   __half2 pair;
@@ -265,7 +266,7 @@ struct Quantised {
 
 // (rarely taken: one copy for all callers)
 template <bool FP16>
-__device__ __noinline__ uint32_t exact_codes(uint4 raw, float s, float m) {
+__device__ __noinline__ uint32_t limited_codes(uint4 raw, float s, float m) {
   float x[8];
   unpack8<FP16>(raw, x);
   uint32_t code = 0;
@@ -303,14 +304,14 @@ __device__ __forceinline__ Quantised quantise(const uint4& raw) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
   const float2 inv2 = make_float2(inv, inv), m2 = make_float2(-m, -m);
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  float worst = fmaxf((m - e.x) * inv, (-e.y - m) * inv - 15.f);
+  const float2 s2 = make_float2(-s, -s);
   uint32_t code = 0;
 #pragma unroll
   for (int i = 3; i >= 0; --i) {
-    const float2 t = mul2(add2(row2_to_float<FP16>(w[i]), m2), inv2);
+    const float2 x = add2(row2_to_float<FP16>(w[i]), m2);
+    float2 t = mul2(x, inv2);
+    t = fma2(fma2(t, s2, x), inv2, t);
     const float2 n = add2(t, make_float2(12582912.f, 12582912.f));  // the integer in the low bits
-    const float2 d = fma2(t, make_float2(-1.f, -1.f), add2(n, make_float2(-12582912.f, -12582912.f)));
-    worst = max3(worst, fabsf(d.x), fabsf(d.y));
     code = (code << 4) + __float_as_uint(n.y);
     code = (code << 4) + __float_as_uint(n.x);
   }
@@ -318,8 +319,8 @@ __device__ __forceinline__ Quantised quantise(const uint4& raw) {
   q.code = code;
   if (!(s > 0.f))
     q.code = 0;
-  else if (worst > 0.49999f)
-    q.code = exact_codes<FP16>(raw, s, m);
+  else if (fmaxf((m - e.x) * inv, (-e.y - m) * inv - 15.f) > 0.4999f)
+    q.code = limited_codes<FP16>(raw, s, m);
   return q;
 }
 
