@@ -445,17 +445,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
       }
       // ---- the largest scale of the tile's values
       float up, down;  // 2^k with s 2^k < 2^14, and 2^-k
-      uint32_t vp[kTile][2][NP];  // V's pairs of the own groups
       {
         __half2 big = __half2half2(__ushort_as_half(0));
 #pragma unroll
         for (int b = 0; b < kTile; ++b) {
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            own_pairs<NP, REP>(vp[b][y], at[b] + 16 * D + ((kKv4Page + row + 8 * y) * NG + rep) * 4);
+            uint32_t vp[NP];
+            own_pairs<NP, REP>(vp, at[b] + 16 * D + ((kKv4Page + row + 8 * y) * NG + rep) * 4);
 #pragma unroll
             for (int u = 0; u < NP; ++u)
-              big = __hmax2(big, __habs2(*reinterpret_cast<__half2*>(&vp[b][y][u])));
+              big = __hmax2(big, __habs2(*reinterpret_cast<__half2*>(&vp[u])));
           }
         }
 #pragma unroll
@@ -470,10 +470,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
       float2 alpha;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float mx = fmaxf(p[0][i], p[0][i + 2]);
+        float mx = top[i];
 #pragma unroll
-        for (int b = 1; b < kTile; ++b) mx = fmaxf(mx, fmaxf(p[b][i], p[b][i + 2]));
-        mx = fmaxf(top[i], rows_max(mx));
+        for (int b = 0; b < kTile; ++b) mx = max3(mx, p[b][i], p[b][i + 2]);
+        mx = rows_max(mx);
         const float base = mx == -INFINITY ? 0.f : mx;
         const float a = ex2((top[i] - base) * F[i]);
         top[i] = mx;
@@ -498,23 +498,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
         float off[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int b = 0; b < kTile; ++b) {
-          const float2 sa = pair(vp[b][0][u]), sb = pair(vp[b][1][u]);
+          uint32_t va[1], vb[1];
+          lds<1>(va, at[b] + 16 * D + ((kKv4Page + row) * NG + u * REP + rep) * 4);
+          lds<1>(vb, at[b] + 16 * D + ((kKv4Page + row + 8) * NG + u * REP + rep) * 4);
+          const float2 sa = pair(va[0]), sb = pair(vb[0]);
           const float ma = fmaf(8.f, sa.x, sa.y), mb = fmaf(8.f, sb.x, sb.y);
           pmt.x = fmaf(p[b][0], ma, fmaf(p[b][2], mb, pmt.x));
           pmt.y = fmaf(p[b][1], ma, fmaf(p[b][3], mb, pmt.y));
           wt[b][0] = transpose8x8(f16x2(p[b][0] * sa.x, p[b][1] * sa.x));
           wt[b][1] = transpose8x8(f16x2(p[b][2] * sb.x, p[b][3] * sb.x));
         }
-        // Rows `row` take whole bytes n0 + 16 n1, rows `row` + 8 the codes 16 n1 in
-        // them; n0 is the difference. Eight for n: -(8 + 128) 2^-24 and -128 2^-24.
+        // every row of `off` is the sum of the tile's rounded weights times -8 / 8: it
+        // counts in each of the eight lanes that hold a part of pm
 #pragma unroll
         for (int b = 0; b < kTile; ++b)
-          mma(off, 0x80888088u, 0x80808080u, 0x80888088u, 0x80808080u, wt[b][0], wt[b][1], off);
-        pm[u] = fma2(pm[u], alpha, mul2(pmt, make_float2(down, down)));
-        // chunks c0 .. of each of the pass's groups; a column's own group counts
+          mma(off, 0xbc00bc00u, 0xbc00bc00u, 0xbc00bc00u, 0xbc00bc00u, wt[b][0], wt[b][1], off);
+        // Chunks c0 .. of each of the pass's groups; a column's own group counts. Rows
+        // `row` take whole bytes n0 + 16 n1, rows `row` + 8 the codes 16 n1 in them; n0
+        // is the difference.
 #pragma unroll
         for (int c0 = 0; c0 < CG; c0 += kPart) {
-          float acc[REP * kPart][2][4];
+          float acc[REP * kPart][2][4], zero[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int b = 0; b < kTile; ++b) {
 #pragma unroll
@@ -527,10 +531,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
               for (int c = 0; c < kPart; ++c) {
                 float(&lo)[4] = acc[y * kPart + c][0], (&hi)[4] = acc[y * kPart + c][1];
                 mma(lo, va[c] & 0x00ff00ffu, va[c] & 0x00f000f0u, vb[c] & 0x00ff00ffu,
-                    vb[c] & 0x00f000f0u, wt[b][0], wt[b][1], b ? lo : off);
+                    vb[c] & 0x00f000f0u, wt[b][0], wt[b][1], b ? lo : zero);
                 const uint32_t a8 = high_bytes(va[c]), b8 = high_bytes(vb[c]);
                 mma(hi, a8, a8 & 0x00f000f0u, b8, b8 & 0x00f000f0u, wt[b][0], wt[b][1],
-                    b ? hi : off);
+                    b ? hi : zero);
               }
             }
           }
@@ -554,6 +558,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
               o[2 * i + 1] = fma2(a[1], c20, mul2(o[2 * i + 1], alpha));
             }
         }
+        pmt = make_float2(pmt.x + off[0], pmt.y + off[1]);
+        pm[u] = fma2(pm[u], alpha, mul2(pmt, make_float2(down, down)));
       }
       __syncwarp();
       issue(nb);

@@ -14,11 +14,11 @@ from __future__ import annotations
 
 import ctypes
 import struct
-from typing import Optional
+from typing import Optional, Sequence
 
 import torch
 
-from .pod_attn import POD_OK, PodError, load_library
+from .pod_attn import POD_OK, PodAttention, PodError, load_library
 
 PAGE_SIZE = 16
 _I32, _U8, _F32 = torch.int32, torch.uint8, torch.float32
@@ -238,6 +238,57 @@ class PodKv4:
         rc = self._lib.pod_kv4_decode(self._h, args.struct, _raw_stream(stream, self.device))
         if rc != POD_OK:
             self._failed(rc, "pod_kv4_decode")
+
+    def hybrid(self, pod: PodAttention, qkv, positions, cos_sin, *, chunk_lens: Sequence[int],
+               prior_lens: Sequence[int], cu_rows, start, ctx_lens, pool, block_table,
+               q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+               stream=None):
+        """One layer's attention of a hybrid batch over the 4-bit cache: the counterpart of
+        :meth:`PodAttention.hybrid` from the projection's output on. Returns O and LSE.
+
+        ``qkv`` [rows, H + 2 Hk, d] holds the chunks of the prefill requests and then one row
+        for each decode; its q and k heads are normed and rotated in place. ``chunk_lens`` and
+        ``prior_lens`` are host lengths as in :meth:`PodAttention.prefill_args`; ``cu_rows``,
+        ``start`` and ``block_table`` cover all requests, the prefills first, and ``ctx_lens``
+        the decodes (their new token included). The new K and V go into the cache; decodes
+        attend over it; the prefills' contexts are read back for ``pod``, a context of the
+        contiguous layout, which takes bf16."""
+        H, Hk, d = self.cfg.num_qo_heads, self.cfg.num_kv_heads, self.cfg.head_dim
+        n_pre, rows = len(chunk_lens), qkv.shape[0]
+        chunk_rows = sum(chunk_lens)
+        if qkv.dim() != 3 or qkv.shape[1:] != (H + 2 * Hk, d):
+            raise ValueError("qkv: expected [rows, num_qo_heads + 2 num_kv_heads, head_dim]")
+        if rows != chunk_rows + ctx_lens.numel() or start.numel() != n_pre + ctx_lens.numel():
+            raise ValueError("qkv, start: expected the chunks' rows and one for each decode")
+        if n_pre and (pod.paged or self.dtype is not torch.bfloat16):
+            raise ValueError("prefills: expected a contiguous-layout context and bfloat16")
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        with torch.cuda.stream(stream):
+            q = torch.empty(rows, H, d, dtype=self.dtype, device=qkv.device)
+            o = torch.empty_like(q)
+            lse = torch.empty(rows, H, dtype=torch.float32, device=qkv.device)
+            k, v = qkv[:, H:H + Hk], qkv[:, H + Hk:]
+            qk_norm_rope(norm_rope_args(qkv[:, :H], k, positions, cos_sin, q_out=q,
+                                        q_weight=q_weight, k_weight=k_weight, eps=eps,
+                                        interleaved=interleaved), stream)
+            self.write(self.rows_args(cu_rows, start, k, v, pool, block_table), stream)
+            if rows > chunk_rows:
+                self.decode(self.decode_args(ctx_lens, q[chunk_rows:], o[chunk_rows:],
+                                             lse[chunk_rows:], pool, block_table[n_pre:]), stream)
+            if chunk_rows:
+                lens = [p + c for p, c in zip(prior_lens, chunk_lens)]
+                cu = torch.tensor([sum(lens[:i]) for i in range(n_pre + 1)] + [0] * n_pre,
+                                  dtype=torch.int32).to(qkv.device)
+                kc = torch.empty(sum(lens), Hk, d, dtype=self.dtype, device=qkv.device)
+                vc = torch.empty_like(kc)
+                self.read(self.rows_args(cu[:n_pre + 1], cu[n_pre + 1:], kc, vc, pool,
+                                         block_table[:n_pre]), stream)
+                pod.prefill_only(pod.prefill_args(list(chunk_lens), list(prior_lens),
+                                                  q[:chunk_rows], o[:chunk_rows],
+                                                  lse[:chunk_rows], k=list(kc.split(lens)),
+                                                  v=list(vc.split(lens))), stream)
+        return o, lse
 
     def _failed(self, rc: int, name: str) -> None:
         _need(self._h is not None, "the context is closed")

@@ -453,6 +453,75 @@ def test_chunked_prefill_over_the_cache():
             assert abs(lse[t, h].item() - torch.logsumexp(sc, 0).item()) <= 1e-3 + size
 
 
+@pytest.mark.parametrize("d,group", [(128, 64), (64, 32)])
+def test_hybrid_batch_over_the_cache(d, group):
+    """PodKv4.hybrid, two steps in a row: chunks and decodes of one batch, each row against the
+    formula over the values that the cache holds after the write."""
+    H, Hk, g = 8, 2, gen(17)
+    kv = p4.PodKv4(H, Hk, d, group_size=group)
+    pod = pa.PodAttention(H, Hk, d, max_prefill_reqs=2, max_prefill_tokens=128, max_decode_reqs=1, max_kv_tokens=512)
+    pool, tab = kv.new_pool(80), p4.rope_table(512, d)
+    w = (1 + 0.1 * torch.randn(d, generator=g)).to(BF).cuda()
+    table = torch.randperm(80, generator=g).reshape(5, 16).to(torch.int32).cuda()
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
+    chunks, done = [50, 13], [0, 0]
+    seen = [0, 3, 40]
+    # the decodes' contexts so far
+    pre = torch.randn(43, 2 * Hk, d, generator=g).to(BF).cuda()
+    kv.write(kv.rows_args(i32([0, 0, 3, 43]), i32([0, 0, 0]), pre[:, :Hk], pre[:, Hk:], pool, table[2:]))
+    for _ in range(2):
+        rows = sum(chunks) + 3
+        qkv = torch.randn(rows, H + 2 * Hk, d, generator=g).to(BF).cuda()
+        before = qkv.clone()
+        pos = i32([p for n, s in zip(chunks, done) for p in range(s, s + n)] + seen)
+        cu = i32([0, chunks[0], sum(chunks)] + [sum(chunks) + 1 + i for i in range(3)])
+        ctx = [n + 1 for n in seen]
+        o, lse = kv.hybrid(pod, qkv, pos, tab, chunk_lens=chunks, prior_lens=done, cu_rows=cu, start=i32(done + seen), ctx_lens=i32(ctx),
+                           pool=pool, block_table=table, q_weight=w, k_weight=w)
+        assert pod.status() == pa.POD_OK
+        q, _ = ref.norm_rope(before[:, :H].cpu(), w.cpu(), tab.cpu(), pos.cpu(), 1e-6, False)
+        q = q.to(BF)
+        check_decode(q[sum(chunks):], pool, table[2:], ctx, d, group, o[sum(chunks):], lse[sum(chunks):])
+        at = 0
+        for r, (n, s) in enumerate(zip(chunks, done)):
+            val = ref.values(pool.cpu()[table.cpu()[r].long()], d, group).permute(2, 1, 0, 3, 4).flatten(2, 3)
+            for t in (0, n // 2, n - 1):
+                for h in (0, H - 1):
+                    kk, vv = val[0, h * Hk // H, :s + t + 1], val[1, h * Hk // H, :s + t + 1]
+                    x = q[at + t, h].double()
+                    sc = kk @ x / math.sqrt(d)
+                    size = (kk.abs() @ x.abs()).max() / math.sqrt(d) * 2.0 ** -8   # as in the test above
+                    assert (o[at + t, h].cpu().double() - torch.softmax(sc, 0) @ vv).abs().max() <= 1e-2 + (2 * size + 2.0 ** -8) * vv.abs().max()
+                    assert abs(lse[at + t, h].item() - torch.logsumexp(sc, 0).item()) <= 1e-3 + size
+            at += n
+        done = [s + n for s, n in zip(done, chunks)]
+        seen = ctx
+    assert pod.close() == pa.POD_OK
+    with pytest.raises(ValueError):
+        kv.hybrid(pod, qkv[:-1], pos, tab, chunk_lens=chunks, prior_lens=done, cu_rows=cu, start=i32(done + seen), ctx_lens=i32(ctx), pool=pool, block_table=table)
+
+
+def test_hybrid_of_decodes_alone_and_of_a_chunk_alone():
+    H, Hk, d = 4, 2, 64
+    kv = p4.PodKv4(H, Hk, d)
+    pod = pa.PodAttention(H, Hk, d, max_prefill_reqs=1, max_prefill_tokens=32, max_decode_reqs=1, max_kv_tokens=64)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
+    tab, table = p4.rope_table(64, d), torch.arange(8, dtype=torch.int32).reshape(2, 4).cuda()
+    x = torch.randn(20, H + 2 * Hk, d, generator=gen(18)).to(BF).cuda()
+    pools = [kv.new_pool(8) for _ in range(2)]
+    # a prompt of 20 tokens as one chunk, and as one chunk of 19 and a decode
+    o, lse = kv.hybrid(pod, x.clone(), i32(list(range(20))), tab, chunk_lens=[20], prior_lens=[0], cu_rows=i32([0, 20]), start=i32([0]),
+                       ctx_lens=i32([]), pool=pools[0], block_table=table[:1])
+    kv.hybrid(pod, x[:19].clone(), i32(list(range(19))), tab, chunk_lens=[19], prior_lens=[0], cu_rows=i32([0, 19]), start=i32([0]),
+              ctx_lens=i32([]), pool=pools[1], block_table=table[:1])
+    o2, lse2 = kv.hybrid(pod, x[19:].clone(), i32([19]), tab, chunk_lens=[], prior_lens=[], cu_rows=i32([0, 1]), start=i32([19]),
+                         ctx_lens=i32([20]), pool=pools[1], block_table=table[:1])
+    assert pod.status() == pa.POD_OK and torch.equal(pools[0], pools[1])
+    # the prefill's tolerance, on outputs of size 1
+    assert (o[19:].float() - o2.float()).abs().max() <= 3e-2 and (lse[19:] - lse2).abs().max() <= 3e-2
+    assert pod.close() == pa.POD_OK
+
+
 def test_calls_with_nothing_to_do():
     kv = p4.PodKv4(4, 2, 64)
     pool = kv.new_pool(1)
