@@ -1,11 +1,12 @@
 // pod_kv4_decode.cu -- single-token GQA attention over the 4-bit KV cache.
 //
-// Bound by the cache's bytes: 16 D + 128 D / group for 16 tokens of one head
-// (2304 at D = 128, groups of 64). At 6.5 TB/s an SM takes one such record in
-// about 100 cycles, so a warp instruction for every 32 pairs of codes costs a
-// sixth of the issue slots and the unpacking decides:
+// Its floor is the cache's bytes: 16 D + 128 D / group for 16 tokens of one head
+// (2304 at D = 128, groups of 64), which an SM's share of 6.5 TB/s brings every
+// 95 cycles. What it costs is taking the codes apart: 4096 codes of such a block
+// are 64 pairs for each lane, so every instruction for a pair is 64 of the
+// block's about 380 issue slots. Hence
 //
-//  * K K^T q as matrix products with the codes themselves. A code n in the low
+//  * K^T q as matrix products with the codes themselves. A code n in the low
 //    bits of an fp16 is the subnormal n 2^-24, exactly: one AND makes two of
 //    them (the codes in bits 4..7 are n 2^-20, undone in the query). The
 //    queries are scaled by a power of two so that their largest channel lies in
@@ -15,22 +16,30 @@
 //    score = s (sum q n) + m (sum q) joins them.
 //  * V^T p as well: rows are channels, columns heads, the same subnormals times
 //    the weights p s, rounded to fp16. What the rounding costs is the weight's
-//    error times n - 8, not n: a product with rows of -8 takes eight of each
-//    rounded weight away, sum p (m + 8 s) in fp32 puts them back unrounded. So that those lie high in fp16, each 64
-//    tokens scale them by a power of two that brings the largest s to [2^13,
-//    2^14): a weight is then off by 2^-11 of itself, or by 2^-39 of the largest
-//    possible one where it is below 2^-28 of that (together below 2^-19 of a
-//    million tokens' weight).
+//    error times n - 8, not n: eight of each rounded weight are taken away and
+//    sum p (m + 8 s) in fp32 puts them back unrounded. So that the weights lie
+//    high in fp16, each 64 tokens scale them by a power of two that brings the
+//    largest s to [2^13, 2^14): a weight is then off by 2^-11 of itself, or by
+//    2^-39 of the largest possible one where it is below 2^-28 of that (together
+//    below 2^-19 of a million tokens' weight). With bf16 weights (2^-8) the error
+//    of an fp16 output was several times that of its own rounding.
 //  * The running maximum and sum, scores, weights and O are fp32; one rescale
 //    every 64 tokens.
 //
 // Work: see pod_kv4_split.h. The line of blocks is cut into equal parts over
 // the CTAs and each of those over its warps, so lengths need no balance and no
-// plan from the host. Warps stream their blocks, one bulk copy each, through rings of their
-// own, across segments. What a warp has of a segment that it does not
-// hold whole is joined first in its CTA, then, where the segment leaves the
+// plan from the host. Warps stream their blocks, one bulk copy each, through
+// rings of their own, across segments. What a warp has of a segment that it does
+// not hold whole is joined first in its CTA, then, where the segment leaves the
 // CTA, through the workspace by the CTA that arrives last, in the order of the
 // tokens: the result does not depend on the order of arrival.
+//
+// Measured on a B200 (L2 not warm): 64 x 4096 tokens of 8 KV heads, G = 4, groups
+// of 64: 72 us, 4.2 TB/s; 16 x 16K..32K, G = 8: 113 us, 4.2 TB/s; 128 x 0.5K..8K,
+// G = 4, groups of 32: 156 us, 4.5 TB/s. The copies alone, with the joins, take
+// 59, 85 and 120 us; with the records in L2 the last but one takes 101, so the
+// instructions bound it: about 225 a block at two an SM and cycle, the integer
+// pipe (the ANDs) 44 % busy, the matrix pipe 28 %.
 #include "pod_kv4.cuh"
 #include "pod_kv4_split.h"
 #include "pod_plan.h"
@@ -39,16 +48,21 @@
 namespace pod {
 namespace {
 
+// 8 warps of up to 255 registers: 12 of 168 issue more at a time, but spill and
+// begin more pieces (113 against 118 us for the long case, 72 against 75 for 64 x
+// 4096), 16 of 128 took 133 and 77.
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 4;   // blocks of 16 tokens between two rescales
-constexpr int kSlots = 8;  // blocks in a warp's ring
+// Blocks of 16 tokens between two rescales: 2 took 127 us for the long case, 4
+// 113, 6 and 8 no less.
+constexpr int kTile = 4;
+constexpr int kSlots = 8;  // blocks in a warp's ring; 10 change nothing, 5 cost 1 %
 constexpr int kKeys = 4;   // blocks whose scores are taken together
 constexpr int kMaxG = 8;
 constexpr int kLeast = 16;  // blocks that make another CTA worth its join
 constexpr float kLn2 = 0.69314718055994531f;
 
-// d = a b + c, one 16 x 16 x 8 product
+// d = a b + c: 16 x 16 times 16 x 8
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                     uint32_t a3, uint32_t b0, uint32_t b1, const float (&c)[4]) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -222,10 +236,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
 
   // Lane i of `cur` has the record of block 32 b + i, of `nxt` that of the 32
   // behind; -1 where the page id lies outside the pool.
+  Kv4Place seg{0, 0, 0, 1};  // of the first block, once every lane has it from lane 0
   const auto records = [&](int base) {
     int rec = 0;
     if (base + lane < total) {
       const Kv4Place p = kv4_place(first, R, Hk, xb + base + lane);
+      if (base == 0) seg = p;
       const int page = __ldg(P.table + (long long)p.r * P.table_stride + p.blk);
       rec = page >= 0 && page < P.pool_blocks ? page * Hk + p.h : -1;
     }
@@ -257,6 +273,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
     islot = islot + count >= kSlots ? islot + count - kSlots : islot + count;
   };
   issue(kSlots);
+  seg.r = __shfl_sync(0xffffffffu, seg.r, 0);
+  seg.h = __shfl_sync(0xffffffffu, seg.h, 0);
+  seg.blk = __shfl_sync(0xffffffffu, seg.blk, 0);
+  seg.nblk = __shfl_sync(0xffffffffu, seg.nblk, 0);
 
   // what the CTA's ends share with others, while the first blocks are on their way
   if (lane == 0 && w < 2) {
@@ -273,7 +293,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
   int slot = 0, phase = 0;  // of the next block
   bool failed = false;
   for (long long x = xb; x < xe;) {
-    const Kv4Place seg = kv4_place(first, R, Hk, x);
+    if (x > xb) {  // the next head, or the next request that is not empty
+      seg.blk = 0;
+      if (++seg.h == Hk) {
+        seg.h = 0;
+        do {
+          ++seg.r;
+          seg.nblk = first[seg.r + 1] - first[seg.r];
+        } while (seg.nblk == 0);
+      }
+    }
     const int n = (int)min((long long)(seg.nblk - seg.blk), xe - x);
     const int len = length(seg.r);
     const long long orow = (long long)seg.r * P.H + (long long)seg.h * G;
@@ -488,7 +517,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
         l[i] = fmaf(l[i], a, s * down);
         (i ? alpha.y : alpha.x) = a;
       }
-      // ---- O
+      // ---- O: where a maximum moved, what is there is scaled first
+      if (__any_sync(0xffffffffu, alpha.x != 1.f || alpha.y != 1.f)) {
+#pragma unroll
+        for (int c = 0; c < NC / REP; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) O[c][i] = mul2(O[c][i], alpha);
+#pragma unroll
+        for (int u = 0; u < NP; ++u) pm[u] = mul2(pm[u], alpha);
+      }
       const float2 c24 = make_float2(down * 0x1p24f, down * 0x1p24f);
       const float2 c20 = make_float2(down * 0x1p20f, down * 0x1p20f);
 #pragma unroll
@@ -554,12 +591,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
               }
               a[0] = fma2(a[1], make_float2(-1.f, -1.f), a[0]);
               float2(&o)[4] = O[u * CG + c0 + c];
-              o[2 * i] = fma2(a[0], c24, mul2(o[2 * i], alpha));
-              o[2 * i + 1] = fma2(a[1], c20, mul2(o[2 * i + 1], alpha));
+              o[2 * i] = fma2(a[0], c24, o[2 * i]);
+              o[2 * i + 1] = fma2(a[1], c20, o[2 * i + 1]);
             }
         }
         pmt = make_float2(pmt.x + off[0], pmt.y + off[1]);
-        pm[u] = fma2(pm[u], alpha, mul2(pmt, make_float2(down, down)));
+        pm[u] = fma2(pmt, make_float2(down, down), pm[u]);
       }
       __syncwarp();
       issue(nb);

@@ -163,7 +163,8 @@ POD_API int pod_kv4_read(pod_kv4_ctx* ctx, const pod_kv4_rows_args* args, void* 
  * as the cache holds them, LSE as in pod_attn.h. Lengths are cut to
  * 0 .. 16 block_table_stride. An empty context gives O = 0 and
  * LSE = -infinity. A request with a page id outside the pool gets O = LSE =
- * NaN. What the cache holds behind a length is never used, whatever its bits.
+ * NaN, and so do the rows of a device-side wait that ran out (after about a
+ * second). What the cache holds behind a length is never used, whatever its bits.
  * The context's workspace serves one call at a time: calls on one context,
  * replays of captured ones included, must not overlap. */
 POD_API int pod_kv4_decode(pod_kv4_ctx* ctx, const pod_kv4_decode_args* args, void* stream);
