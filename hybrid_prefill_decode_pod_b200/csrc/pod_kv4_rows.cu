@@ -35,6 +35,10 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 // them with its weights once, y_i = inv (x_i a_i + x_partner b_i), and a head
 // costs two multiply-adds for each channel. The partner, rot / 2 channels away,
 // comes by shuffle as it was read.
+//
+// 16384 rows of 72 heads of 128: 105 us, 5.8 TB/s, 90 % of the copy rate, at four
+// CTAs an SM (64 registers); three CTAs took 115, batches of 3 or 6 at four 115
+// and 118, of 2 at five 108.
 constexpr int kBatch = 4;
 
 template <int D, bool FP16, bool INTERLEAVED>
@@ -343,6 +347,11 @@ __device__ __forceinline__ uint4 values(uint32_t code, uint32_t sm) {
 // Bound by the rows' bytes, D bytes of codes for 4 D of K and V. A whole page is
 // put together in shared memory, since V's codes of a token lie 16 bytes apart,
 // and leaves in 16-byte pieces; part of a page goes to its places directly.
+//
+// 16384 tokens of 8 heads of 128: 30 us for 85 MB (13 at the copy rate): 300 warp
+// instructions for four rows of K or V each, two thirds of the issue slots, in
+// 1.7 waves of CTAs. Two steps in flight at four CTAs an SM; three steps, or
+// five or six CTAs with fewer registers, took 1 to 10 % more.
 template <int D, int GROUP, bool FP16>
 __global__ void __launch_bounds__(kThreads, 4) kv4_write_kernel(const Kv4Rows P) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, NG = D / GROUP;
@@ -402,7 +411,8 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_write_kernel(const Kv4Rows P)
 }
 
 // The reverse: the record comes to shared memory in 16-byte pieces, the rows
-// leave in 16 bytes a lane.
+// leave in 16 bytes a lane. 11264 tokens of 8 heads of 128: 17 us for 86 MB (13 at
+// the copy rate), 1.7 waves of CTAs again.
 template <int D, int GROUP, bool FP16>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Rows P) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, NG = D / GROUP;

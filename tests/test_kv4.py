@@ -57,8 +57,11 @@ def row_places(lens, starts, table):
     return out
 
 
+# (the last two: more than 31 requests end in 16 rows, and more than 33 * 33 requests)
 LENS = [([1], [0]), ([1, 1, 1, 1, 1], [15, 16, 0, 31, 77]), ([16, 32], [0, 16]),
-        ([0, 5, 0, 40, 17, 0], [3, 14, 0, 8, 1, 0]), ([100, 1, 16], [7, 1000, 9])]
+        ([0, 5, 0, 40, 17, 0], [3, 14, 0, 8, 1, 0]), ([100, 1, 16], [7, 1000, 9]),
+        ([0] * 40 + [3] + [0] * 70 + [2, 1] + [0] * 5, [0] * 40 + [14] + [0] * 70 + [2, 0] + [7] * 5),
+        ([0, 1] * 20 + [0] * 1200 + [18] + [0] * 3, [i % 48 for i in range(40)] + [0] * 1200 + [13] + [0] * 3)]
 
 
 @pytest.mark.parametrize("dtype", [BF, HF])
@@ -234,6 +237,57 @@ def test_decode_matches_the_formula(lens, H, Hk, d, group, dtype):
     check_decode(q, pool, table, lens, d, group, o, lse)
     again = run_decode(kv, qc, pc, tc, lc)   # the order of the parts does not change a bit
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("R,H,Hk", [(4096, 2, 1), (1500, 3, 3)])
+def test_decode_of_many_short_requests(R, H, Hk):
+    """More requests than threads, empty ones among them; the largest number a context admits."""
+    lens = [(7 * i) % 5 * (i % 3) for i in range(R)]
+    lens[R // 2] = 300
+    q, pool, table = decode_case(lens, H, Hk, 64, 32, BF, 19)
+    kv = p4.PodKv4(H, Hk, 64, group_size=32, max_decode_reqs=R)
+    o, lse = run_decode(kv, q.cuda(), pool.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda())
+    check_decode(q, pool, table, lens, 64, 32, o, lse)
+
+
+def test_shared_pages_may_be_read_by_many():
+    """A common prefix: several requests list the same pages, also twice in one row."""
+    d, group, H, Hk = 128, 64, 4, 2
+    q, pool, table = decode_case([64, 64, 64], H, Hk, d, group, BF, 20)
+    table[1] = table[0]
+    table[2, 1:] = table[2, :1]
+    lens = [64, 50, 64]
+    kv = p4.PodKv4(H, Hk, d, group_size=group)
+    o, lse = run_decode(kv, q.cuda(), pool.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda())
+    check_decode(q, pool, table, lens, d, group, o, lse)
+    cu, start = torch.tensor([0, 64, 114, 178], dtype=torch.int32).cuda(), torch.zeros(3, dtype=torch.int32).cuda()
+    k, v = (torch.zeros(178, Hk, d, dtype=BF, device="cuda") for _ in range(2))
+    kv.read(kv.rows_args(cu, start, k, v, pool.cuda(), table.cuda()))
+    assert torch.equal(k[64:114], k[:50]) and torch.equal(v[114:130], v[130:146])
+
+
+def test_two_graphs_on_one_context_replayed_in_turn():
+    """They share the workspace, one after the other on one stream."""
+    cases = [decode_case(lens, 8, 1, 128, 128, HF, 21 + i) for i, lens in enumerate(([5000, 40], [900] * 7))]
+    kv, graphs, outs = p4.PodKv4(8, 1, 128, group_size=128, dtype=HF), [], []
+    held = []
+    for (q, pool, table), lens in zip(cases, ([5000, 40], [900] * 7)):
+        args = [q.cuda(), pool.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()]
+        run_decode(kv, *args)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = run_decode(kv, *args)
+        held.append(args)
+        graphs.append(g)
+        outs.append(out)
+    for i in (0, 1, 1, 0, 1):
+        outs[i][0].fill_(7)
+        graphs[i].replay()
+    for out, args, lens, (q, pool, table) in zip(outs, held, ([5000, 40], [900] * 7), cases):
+        eager = run_decode(kv, *args)
+        assert torch.equal(out[0], eager[0]) and torch.equal(out[1], eager[1])
+        check_decode(q, pool, table, lens, 128, 128, *eager)
 
 
 def test_decode_extreme_queries():
