@@ -40,6 +40,8 @@
 // 59, 85 and 120 us; with the records in L2 the last but one takes 101, so the
 // instructions bound it: about 225 a block at two an SM and cycle, the integer
 // pipe (the ANDs) 44 % busy, the matrix pipe 28 %.
+#include <algorithm>
+
 #include "pod_kv4.cuh"
 #include "pod_kv4_split.h"
 #include "pod_plan.h"
@@ -60,6 +62,11 @@ constexpr int kSlots = 8;  // blocks in a warp's ring; 10 change nothing, 5 cost
 constexpr int kKeys = 4;   // blocks whose scores are taken together
 constexpr int kMaxG = 8;
 constexpr int kLeast = 16;  // blocks that make another CTA worth its join
+// Up to this many blocks in the longest context (1024 tokens) a segment stays in
+// one CTA: the joins between CTAs take about 4 us, in which a CTA does some 64
+// blocks. 16 x 1000 tokens, 8 KV heads: 16.2 us cut anywhere, KWHOLE_A whole; 8 x 100:
+// 13.7 and KWHOLE_B.
+constexpr int kWhole = 64;
 constexpr float kLn2 = 0.69314718055994531f;
 
 // d = a b + c: 16 x 16 times 16 x 8
@@ -187,17 +194,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
   const auto length = [&](int r) { return (int)min((long long)max(__ldg(P.ctx_lens + r), 0), cap); };
 
   // first[r]: blocks of one head in front of request r
+  int longest = 0;
   {
     const int each = (R + kThreads - 1) / kThreads, r0 = min(tid * each, R), r1 = min(r0 + each, R);
-    int sum = 0;
-    for (int r = r0; r < r1; ++r) sum += (length(r) + 15) >> 4;
+    int sum = 0, big = 0;
+    for (int r = r0; r < r1; ++r) {
+      const int n = (length(r) + 15) >> 4;
+      sum += n;
+      big = max(big, n);
+    }
+    big = __reduce_max_sync(0xffffffffu, big);
     int inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
-    if (lane == 31) misc[w] = inc;
+    if (lane == 31) {
+      misc[w] = inc;
+      misc[kWarps + w] = big;
+    }
     if (tid < kWarps) meta[tid].has[0] = meta[tid].has[1] = 0;
     if (tid < kWarps * kSlots) mbar_init(smem_u32(smem + S::kBarOff) + tid * 8, 1);
     fence_mbar_init();
@@ -206,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
     __syncthreads();
     int before = inc - sum;
     for (int x = 0; x < w; ++x) before += misc[x];
+    for (int x = 0; x < kWarps; ++x) longest = max(longest, misc[kWarps + x]);
     for (int r = r0; r < r1; ++r) {
       first[r] = before;
       before += (length(r) + 15) >> 4;
@@ -223,11 +240,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
     for (int i = tid; i < P.H; i += kThreads) P.lse[(long long)r * P.H + i] = -INFINITY;
   }
   if (W == 0) return;
-  const int N = kv4_workers(W, gridDim.x, kLeast), cta = blockIdx.x;
+  const bool whole = longest <= kWhole;
+  const int cta = blockIdx.x, least = kv4_workers(W, gridDim.x, kLeast);
+  const int N = whole ? max(least, (int)min((long long)R * Hk, (long long)gridDim.x)) : least;
   if (cta >= N) return;
 
   // ------------------------------------------------ this warp's blocks
-  const long long cb = kv4_begin(W, N, cta), ce = kv4_begin(W, N, cta + 1);
+  long long cb = kv4_begin(W, N, cta), ce = kv4_begin(W, N, cta + 1);
+  if (whole) {
+    cb = kv4_snap(first, R, Hk, W, cb);
+    ce = kv4_snap(first, R, Hk, W, ce);
+    if (cb == ce) return;
+  }
   const long long xb = cb + kv4_begin(ce - cb, kWarps, w), xe = cb + kv4_begin(ce - cb, kWarps, w + 1);
   const int total = (int)(xe - xb);
   unsigned char* ring = smem + w * S::kRing;
@@ -780,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
       const int g = i / (D / 4);
       float mx = -INFINITY, sum = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
       for (int c = m.c0; c <= m.c1; ++c) {
         const float* part =
             P.part + ((long long)c * (2 + kWarps) + (c == m.c0 ? 1 : 0)) * part_stride;
@@ -842,7 +866,8 @@ cudaError_t launch_kv4_decode(const Kv4Decode& P, int D, int group, int dtype, c
   const Choice c = choose(D, group, dtype, P.G);
   // no more CTAs than the tables could give work to
   const long long most = (long long)P.num_reqs * P.table_stride * P.Hk;
-  const int grid = kv4_workers(most, P.grid, kLeast);
+  const int grid = std::max(kv4_workers(most, P.grid, kLeast),
+                            (int)std::min((long long)P.num_reqs * P.Hk, (long long)P.grid));
   c.kernel<<<grid, kThreads, c.smem(P.num_reqs), s>>>(P);
   return cudaGetLastError();
 }

@@ -4,7 +4,9 @@
 // The W = Hk * sum(blocks) blocks of 16 tokens, in the order (request, KV head,
 // block), are one line that N workers cut into equal lengths: worker c takes
 // [c W / N, (c + 1) W / N). A (request, KV head) is a segment of that line and
-// may lie in several workers. With N <= W every worker has a block.
+// may lie in several workers. With N <= W every worker has a block. Where all
+// segments are short the cuts move to the next boundary between two, so that no
+// segment lies in several workers; a worker may then have none.
 #pragma once
 
 namespace pod {
@@ -48,6 +50,13 @@ POD_HD Kv4Place kv4_place(const int* first, int R, int Hk, long long x) {
   p.h = (int)kv4_div(rem, p.nblk);
   p.blk = (int)(rem - (long long)p.h * p.nblk);
   return p;
+}
+
+// The segment boundary next to x, 0 <= x <= W.
+POD_HD long long kv4_snap(const int* first, int R, int Hk, long long W, long long x) {
+  if (x >= W) return W;
+  const Kv4Place p = kv4_place(first, R, Hk, x);
+  return 2 * p.blk <= p.nblk ? x - p.blk : x + (p.nblk - p.blk);
 }
 
 // Workers of a call: no more than there are CTAs, each with at least

@@ -200,6 +200,13 @@ def test_work_is_cut_into_equal_whole_parts(harness, lens, Hk, ctas, least):
         assert at[c] <= x < at[c + 1]
         harness.harness_place(first, len(lens), Hk, x, out)
         assert tuple(out) == want[x]
+    # cuts moved to the boundary next to them: in order, and by no more than half a segment
+    harness.harness_snap.restype = ll
+    harness.harness_snap.argtypes = [ctypes.POINTER(i32), i32, i32, ll, ll]
+    ends = sorted({0} | {x + n - b for x, (_, _, b, n) in enumerate(want)})
+    moved = [harness.harness_snap(first, len(lens), Hk, W, b) for b in at]
+    assert moved[0] == 0 and moved[-1] == W and moved == sorted(moved) and set(moved) <= set(ends)
+    assert all(2 * abs(m - b) <= max(lens) for m, b in zip(moved, at))
 
 
 def test_work_of_the_largest_calls(harness):
