@@ -57,7 +57,7 @@ int check_cache(const pod_kv4_ctx* c, int num_reqs, const void* pool, long long 
   if (!pool || (!table && stride) || blocks <= 0 || stride < 0) return POD_EINVAL;
   if (!aligned16(pool) || !aligned4(table)) return POD_EINVAL;
   if (blocks * c->cfg.num_kv_heads > (1LL << 31) - 1 || blocks > (1LL << 31) - 1 ||
-      (long long)num_reqs * stride > (1LL << 31) - 1 || stride > (1 << 26))
+      (long long)num_reqs * (stride + 8LL) > (1LL << 31) - 1 || stride > (1 << 26))
     return POD_ECAPACITY;
   return POD_OK;
 }

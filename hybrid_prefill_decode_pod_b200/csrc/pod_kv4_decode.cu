@@ -26,9 +26,10 @@
 //  * The running maximum and sum, scores, weights and O are fp32; one rescale
 //    every 64 tokens.
 //
-// Work: see pod_kv4_split.h. The line of blocks is cut into equal parts over
-// the CTAs and each of those over its warps, so lengths need no balance and no
-// plan from the host. Warps stream their blocks, one bulk copy each, through
+// Work: see pod_kv4_split.h. The line of blocks is cut into parts of equal cost
+// over the CTAs and each of those over its warps, so lengths need no balance and
+// no plan from the host. (Cut into equal numbers of blocks, 256 contexts of 1 to
+// 1000 tokens took 83 us, in order of length 160; by cost 46 and 47.) Warps stream their blocks, one bulk copy each, through
 // rings of their own, across segments. What a warp has of a segment that it does
 // not hold whole is joined first in its CTA, then, where the segment leaves the
 // CTA, through the workspace by the CTA that arrives last, in the order of the
@@ -64,8 +65,8 @@ constexpr int kMaxG = 8;
 constexpr int kLeast = 16;  // blocks that make another CTA worth its join
 // Up to this many blocks in the longest context (1024 tokens) a segment stays in
 // one CTA: the joins between CTAs take about 4 us, in which a CTA does some 64
-// blocks. 16 x 1000 tokens, 8 KV heads: 16.2 us cut anywhere, KWHOLE_A whole; 8 x 100:
-// 13.7 and KWHOLE_B.
+// blocks. 16 x 1000 tokens, 8 KV heads: 16.2 us cut anywhere, 12.3 whole; 8 x 100:
+// 13.7 and 9.4.
 constexpr int kWhole = 64;
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -159,11 +160,11 @@ struct Shape {
   static constexpr int kMlOff = kWarps * kRing;  // float [warp][2][kMaxG][2]
   static constexpr int kMetaOff = kMlOff + kWarps * 2 * kMaxG * 2 * 4;
   static constexpr int kMiscOff = kMetaOff + kWarps * (int)sizeof(PieceMeta);
-  static constexpr int kBarOff = (kMiscOff + 2 * kWarps * 4 + 2 * (int)sizeof(Shared) + 7) / 8 * 8;  // mbarrier [warp][slot]
+  static constexpr int kBarOff = (kMiscOff + 3 * kWarps * 4 + 2 * (int)sizeof(Shared) + 7) / 8 * 8;  // mbarrier [warp][slot]
   // a record whose pairs are 0, for a tile of fewer than kTile blocks
   static constexpr int kZeroOff = (kBarOff + kWarps * kSlots * 8 + 15) / 16 * 16;
   static constexpr int kFirstOff = kZeroOff + kRec;
-  static __host__ int smem(int reqs) { return kFirstOff + (reqs + 1) * 4; }
+  static __host__ int smem(int reqs) { return kFirstOff + 2 * (reqs + 1) * 4; }
 };
 
 // REP: how often each head stands among the eight columns of the products
@@ -181,8 +182,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
   float* ml = reinterpret_cast<float*>(smem + S::kMlOff);
   PieceMeta* meta = reinterpret_cast<PieceMeta*>(smem + S::kMetaOff);
   int* misc = reinterpret_cast<int*>(smem + S::kMiscOff);
-  Shared* out = reinterpret_cast<Shared*>(misc + 2 * kWarps);
+  Shared* out = reinterpret_cast<Shared*>(misc + 3 * kWarps);
   int* first = reinterpret_cast<int*>(smem + S::kFirstOff);
+  int* cost = first + P.num_reqs + 1;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, row = lane >> 2, j = lane & 3;
   // the replica and the heads of this lane's columns 2 j and 2 j + 1
   const int rep = REP == 1 ? 0 : REP == 2 ? j >> 1 : j, head0 = 2 * j % (8 / REP);
@@ -193,26 +195,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
   const long long cap = min((long long)P.table_stride * kKv4Page, (1LL << 31) - 16);
   const auto length = [&](int r) { return (int)min((long long)max(__ldg(P.ctx_lens + r), 0), cap); };
 
-  // first[r]: blocks of one head in front of request r
+  // first[r], cost[r]: blocks of one head in front of request r, and their cost
   int longest = 0;
   {
     const int each = (R + kThreads - 1) / kThreads, r0 = min(tid * each, R), r1 = min(r0 + each, R);
-    int sum = 0, big = 0;
+    int sum = 0, sum_c = 0, big = 0;
     for (int r = r0; r < r1; ++r) {
       const int n = (length(r) + 15) >> 4;
       sum += n;
+      sum_c += kv4_cost(n);
       big = max(big, n);
     }
     big = __reduce_max_sync(0xffffffffu, big);
-    int inc = sum;
+    int inc = sum, inc_c = sum_c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
+      const int y = __shfl_up_sync(0xffffffffu, inc, o), z = __shfl_up_sync(0xffffffffu, inc_c, o);
+      if (lane >= o) {
+        inc += y;
+        inc_c += z;
+      }
     }
     if (lane == 31) {
       misc[w] = inc;
-      misc[kWarps + w] = big;
+      misc[kWarps + w] = inc_c;
+      misc[2 * kWarps + w] = big;
     }
     if (tid < kWarps) meta[tid].has[0] = meta[tid].has[1] = 0;
     if (tid < kWarps * kSlots) mbar_init(smem_u32(smem + S::kBarOff) + tid * 8, 1);
@@ -220,14 +227,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
     for (int i = tid; i < kRec / 4; i += kThreads)
       reinterpret_cast<uint32_t*>(smem + S::kZeroOff)[i] = 0;
     __syncthreads();
-    int before = inc - sum;
-    for (int x = 0; x < w; ++x) before += misc[x];
-    for (int x = 0; x < kWarps; ++x) longest = max(longest, misc[kWarps + x]);
-    for (int r = r0; r < r1; ++r) {
-      first[r] = before;
-      before += (length(r) + 15) >> 4;
+    int before = inc - sum, before_c = inc_c - sum_c;
+    for (int x = 0; x < kWarps; ++x) {
+      if (x < w) {
+        before += misc[x];
+        before_c += misc[kWarps + x];
+      }
+      longest = max(longest, misc[2 * kWarps + x]);
     }
-    if (tid == kThreads - 1) first[R] = before;
+    for (int r = r0; r < r1; ++r) {
+      const int n = (length(r) + 15) >> 4;
+      first[r] = before;
+      cost[r] = before_c;
+      before += n;
+      before_c += kv4_cost(n);
+    }
+    if (tid == kThreads - 1) {
+      first[R] = before;
+      cost[R] = before_c;
+    }
     __syncthreads();
   }
   const long long W = (long long)first[R] * Hk;
@@ -242,17 +260,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
   if (W == 0) return;
   const bool whole = longest <= kWhole;
   const int cta = blockIdx.x, least = kv4_workers(W, gridDim.x, kLeast);
-  const int N = whole ? max(least, (int)min((long long)R * Hk, (long long)gridDim.x)) : least;
+  // A segment of n blocks in p parts costs about n / p times 0.055 us and p times
+  // 0.09 us for the join of the parts: p up to sqrt(0.6 n). One context of 30000
+  // tokens of one KV head in 117 parts: 21 us, in 34 16 us.
+  const long long parts = (long long)R * Hk * max(1, (int)sqrtf(0.6f * longest));
+  const int N = whole ? max(least, (int)min((long long)R * Hk, (long long)gridDim.x))
+                      : (int)min((long long)least, parts);
   if (cta >= N) return;
 
   // ------------------------------------------------ this warp's blocks
-  long long cb = kv4_begin(W, N, cta), ce = kv4_begin(W, N, cta + 1);
-  if (whole) {
-    cb = kv4_snap(first, R, Hk, W, cb);
-    ce = kv4_snap(first, R, Hk, W, ce);
-    if (cb == ce) return;
-  }
-  const long long xb = cb + kv4_begin(ce - cb, kWarps, w), xe = cb + kv4_begin(ce - cb, kWarps, w + 1);
+  const long long V = (long long)cost[R] * Hk;
+  // lane 0 looks up the beginning, lane 1 the end
+  const int end_lane = min(lane, 1);
+  long long v = kv4_begin(V, N, cta + end_lane);
+  if (whole) v = kv4_snap(cost, R, Hk, v);
+  long long x_of = kv4_cut(first, cost, R, Hk, v);
+  const long long vb = __shfl_sync(0xffffffffu, v, 0), ve = __shfl_sync(0xffffffffu, v, 1);
+  const long long cb = __shfl_sync(0xffffffffu, x_of, 0), ce = __shfl_sync(0xffffffffu, x_of, 1);
+  if (cb == ce) return;
+  // The warps take equal numbers of blocks where the CTA has few segments (each
+  // warp begins a piece anyway), equal costs where it has more than warps.
+  if (ve - vb - (ce - cb) <= kKv4Start * kWarps)
+    x_of = cb + kv4_begin(ce - cb, kWarps, w + end_lane);
+  else
+    x_of = kv4_cut(first, cost, R, Hk, vb + kv4_begin(ve - vb, kWarps, w + end_lane));
+  const long long xb = __shfl_sync(0xffffffffu, x_of, 0), xe = __shfl_sync(0xffffffffu, x_of, 1);
   const int total = (int)(xe - xb);
   unsigned char* ring = smem + w * S::kRing;
   const uint32_t ring_s = smem_u32(ring), bar_s = smem_u32(smem + S::kBarOff) + w * kSlots * 8,
@@ -308,8 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
     const long long x0 = (long long)Hk * first[p.r] + (long long)p.h * p.nblk;
     Shared m{p.r, p.h, 0, 0};
     if (w ? x0 >= cb && x0 + p.nblk > ce : x0 < cb) {
-      m.c0 = kv4_worker(W, N, x0);
-      m.c1 = kv4_worker(W, N, x0 + p.nblk - 1);
+      m.c0 = kv4_worker(cost, R, Hk, N, p.r, p.h, 0);
+      m.c1 = kv4_worker(cost, R, Hk, N, p.r, p.h, p.nblk - 1);
     }
     out[w] = m;
   }
@@ -337,7 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
     float qs[NP][2], F[2];
     {
       const int q_head = row % (8 / REP), q_rep = row / (8 / REP);
-      float q[NC][8], big = 0.f;
+      float q[NC][8];
+      uint32_t most = 0;  // the largest magnitudes, in the queries' own type
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         uint4 v = make_uint4(0, 0, 0, 0);
@@ -349,13 +382,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
           const float2 f = row2_to_float<FP16>(vv[i]);
           q[c][2 * i] = f.x;
           q[c][2 * i + 1] = f.y;
-          big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
-          if (!(fabsf(f.x) < INFINITY && fabsf(f.y) < INFINITY)) big = INFINITY;
+          most = max2<FP16>(most, vv[i] & 0x7fff7fffu);
         }
       }
-      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-      const int e = __float_as_int(big) >> 23;
+      most = max2<FP16>(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = max2<FP16>(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      most = max2<FP16>(most, most >> 16);
+      const int e = __float_as_int(row2_to_float<FP16>(most).x) >> 23;  // 255 for NaN too
       const float sc = e == 0 || e == 255 ? 1.f : __int_as_float(min(263 - e, 254) << 23);
       const float f = P.scale_log2 * 16777216.f / sc;
       float sum[NP];
@@ -384,6 +417,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
       F[0] = __shfl_sync(0xffffffffu, f, 8 * j);
       F[1] = __shfl_sync(0xffffffffu, f, 8 * j + 4);
     }
+
+    // the next segment's queries come closer meanwhile (they follow on, empty requests apart)
+    if (x + n < xe && lane * 64 < G * D)
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(P.q + min((orow + G) * D + lane * 64, (long long)R * P.H * D - 8)));
 
     // State of heads head0 (x) and head0 + 1 (y): O of channels 4 row + 0..3 of the
     // own groups' chunks, this lane's part of the sums of p and of p (m + 8 s).

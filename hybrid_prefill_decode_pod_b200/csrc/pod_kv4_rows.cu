@@ -233,26 +233,6 @@ __device__ __forceinline__ void for_pages(const Kv4Rows& P, F f) {
   }
 }
 
-// Least or largest (NaN if either is) of two values each.
-template <bool FP16>
-__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  if constexpr (FP16)
-    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  else
-    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-template <bool FP16>
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  if constexpr (FP16)
-    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  else
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 // Codes of a lane's eight values, and the pair of their group, which GROUP / 8
 // adjacent lanes share (all lanes of the warp call this).
 //

@@ -2,11 +2,15 @@
 // the host tests.
 //
 // The W = Hk * sum(blocks) blocks of 16 tokens, in the order (request, KV head,
-// block), are one line that N workers cut into equal lengths: worker c takes
-// [c W / N, (c + 1) W / N). A (request, KV head) is a segment of that line and
-// may lie in several workers. With N <= W every worker has a block. Where all
-// segments are short the cuts move to the next boundary between two, so that no
-// segment lies in several workers; a worker may then have none.
+// block), are one line; a (request, KV head) is a segment of it. N workers cut
+// the line into parts of equal cost: a segment of n blocks costs what its tiles
+// of four blocks cost and kv4_start blocks more for its queries and its end. The
+// cuts are therefore made on a second line, of costs, on which worker c takes
+// [c V / N, (c + 1) V / N), and carried over to the blocks.
+//
+// A segment may lie in several workers. Where all segments are short the cuts
+// move to the next boundary between two, so that none does; a worker may then
+// have no block.
 #pragma once
 
 namespace pod {
@@ -21,15 +25,15 @@ namespace pod {
 POD_HD long long kv4_div(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
-POD_HD long long kv4_begin(long long W, int N, int c) { return kv4_div(c * W, N); }
 
-// The worker that holds block x: the largest c with c W / N <= x.
-POD_HD int kv4_worker(long long W, int N, long long x) {
-  return (int)kv4_div((x + 1) * N - 1, W);
-}
+// What a segment of n blocks costs: its tiles, and `start` before them.
+constexpr int kKv4Start = 4;
+POD_HD int kv4_cost(int n) { return n ? ((n + 3) & ~3) + kKv4Start : 0; }
 
-// Where block x of the line lies: first[r] is the number of blocks of one head
-// in front of request r (first[R] their sum), 0 <= x < Hk * first[R].
+POD_HD long long kv4_begin(long long V, int N, int c) { return kv4_div(c * V, N); }
+
+// Where x of a line lies: first[r] is the length of one head of the requests in
+// front of r (first[R] of all), 0 <= x < Hk * first[R].
 struct Kv4Place {
   int r, h, blk, nblk;
 };
@@ -52,11 +56,27 @@ POD_HD Kv4Place kv4_place(const int* first, int R, int Hk, long long x) {
   return p;
 }
 
-// The segment boundary next to x, 0 <= x <= W.
-POD_HD long long kv4_snap(const int* first, int R, int Hk, long long W, long long x) {
-  if (x >= W) return W;
-  const Kv4Place p = kv4_place(first, R, Hk, x);
-  return 2 * p.blk <= p.nblk ? x - p.blk : x + (p.nblk - p.blk);
+// The segment boundary next to v on the line of costs, 0 <= v <= Hk * cost[R].
+POD_HD long long kv4_snap(const int* cost, int R, int Hk, long long v) {
+  if (v >= (long long)Hk * cost[R]) return (long long)Hk * cost[R];
+  const Kv4Place p = kv4_place(cost, R, Hk, v);
+  return 2 * p.blk <= p.nblk ? v - p.blk : v + (p.nblk - p.blk);
+}
+
+// The first block behind the cut at v of the line of costs. first and cost: blocks
+// and costs of one head in front of each request.
+POD_HD long long kv4_cut(const int* first, const int* cost, int R, int Hk, long long v) {
+  if (v >= (long long)Hk * cost[R]) return (long long)Hk * first[R];
+  const Kv4Place p = kv4_place(cost, R, Hk, v);
+  const int n = first[p.r + 1] - first[p.r], blk = p.blk - kKv4Start;
+  return (long long)Hk * first[p.r] + (long long)p.h * n + (blk < 0 ? 0 : blk > n ? n : blk);
+}
+
+// The worker that holds block blk of (r, h), where cuts are not moved.
+POD_HD int kv4_worker(const int* cost, int R, int Hk, int N, int r, int h, int blk) {
+  const long long V = (long long)Hk * cost[R];
+  const long long v = (long long)Hk * cost[r] + (long long)h * (cost[r + 1] - cost[r]) + kKv4Start + blk;
+  return (int)kv4_div((v + 1) * N - 1, V);
 }
 
 // Workers of a call: no more than there are CTAs, each with at least

@@ -24,10 +24,12 @@ POD_API pod_kv4_ctx* harness_ctx(const pod_kv4_config* cfg) {
   c->cfg = *cfg;
   return c;
 }
-POD_API long long harness_begin(long long W, int N, int c) { return kv4_begin(W, N, c); }
-POD_API int harness_worker(long long W, int N, long long x) { return kv4_worker(W, N, x); }
+POD_API long long harness_begin(long long V, int N, int c) { return kv4_begin(V, N, c); }
+POD_API int harness_cost(int n) { return kv4_cost(n); }
 POD_API int harness_workers(long long W, int ctas, int least) { return kv4_workers(W, ctas, least); }
-POD_API long long harness_snap(const int* first, int R, int Hk, long long W, long long x) { return kv4_snap(first, R, Hk, W, x); }
+POD_API long long harness_snap(const int* cost, int R, int Hk, long long v) { return kv4_snap(cost, R, Hk, v); }
+POD_API long long harness_cut(const int* first, const int* cost, int R, int Hk, long long v) { return kv4_cut(first, cost, R, Hk, v); }
+POD_API int harness_worker(const int* cost, int R, int Hk, int N, int r, int h, int blk) { return kv4_worker(cost, R, Hk, N, r, h, blk); }
 POD_API void harness_place(const int* first, int R, int Hk, long long x, int* out) {
   const Kv4Place p = kv4_place(first, R, Hk, x);
   out[0] = p.r; out[1] = p.h; out[2] = p.blk; out[3] = p.nblk;

@@ -177,49 +177,89 @@ def test_norm_rope_refused(harness, kw, code):
     assert rc == code if code is not None else rc in PAST_THE_CHECKS
 
 
-@pytest.mark.parametrize("lens,Hk", [([1], 1), ([0, 5, 0, 0, 17, 1, 0], 3), ([100] * 9, 8), ([4000, 1], 2), ([0, 0, 33], 5)])
-@pytest.mark.parametrize("ctas,least", [(148, 16), (7, 1), (1, 16), (296, 4)])
-def test_work_is_cut_into_equal_whole_parts(harness, lens, Hk, ctas, least):
-    """Every block belongs to one worker, the parts differ by one block, and a block's place is its own."""
-    ll, i32 = ctypes.c_longlong, ctypes.c_int
-    harness.harness_begin.restype = ll
-    harness.harness_begin.argtypes = [ll, i32, i32]
-    harness.harness_worker.argtypes = [ll, i32, ll]
-    harness.harness_workers.argtypes = [ll, i32, i32]
-    harness.harness_place.argtypes = [ctypes.POINTER(i32), i32, i32, ll, ctypes.POINTER(i32)]
-    first = (i32 * (len(lens) + 1))(*[sum(lens[:i]) for i in range(len(lens) + 1)])
-    W = sum(lens) * Hk
-    N = harness.harness_workers(W, ctas, least)
-    assert 1 <= N <= ctas and (N == 1 or W // N >= least)
-    at = [harness.harness_begin(W, N, c) for c in range(N + 1)]
-    assert at[0] == 0 and at[-1] == W and max(b - a for a, b in zip(at, at[1:])) <= W // N + 1
+@pytest.fixture(scope="module")
+def split(harness):
+    """pod_kv4_split.h's functions over a batch: blocks of each request and the KV heads."""
+    ll, i32, ptr = ctypes.c_longlong, ctypes.c_int, ctypes.POINTER(ctypes.c_int)
+    for name, res, args in (("begin", ll, [ll, i32, i32]), ("cost", i32, [i32]), ("workers", i32, [ll, i32, i32]), ("snap", ll, [ptr, i32, i32, ll]),
+                            ("cut", ll, [ptr, ptr, i32, i32, ll]), ("worker", i32, [ptr, i32, i32, i32, i32, i32, i32]),
+                            ("place", None, [ptr, i32, i32, ll, ptr])):
+        f = getattr(harness, "harness_" + name)
+        f.restype, f.argtypes = res, args
+    return harness
+
+
+def prefix(xs):
+    return (ctypes.c_int * (len(xs) + 1))(*[sum(xs[:i]) for i in range(len(xs) + 1)])
+
+
+BATCHES = [([1], 1), ([0, 5, 0, 0, 17, 1, 0], 3), ([100] * 9, 8), ([4000, 1], 2), ([0, 0, 33], 5), ([1, 2, 3, 4, 5, 6, 7, 64] * 5, 2)]
+
+
+@pytest.mark.parametrize("lens,Hk", BATCHES)
+def test_places_on_the_line(split, lens, Hk):
+    first, out = prefix(lens), (ctypes.c_int * 4)()
     want = [(r, h, b, n) for r, n in enumerate(lens) for h in range(Hk) for b in range(n)]
-    out = (i32 * 4)()
-    for x in range(W):
-        c = harness.harness_worker(W, N, x)
-        assert at[c] <= x < at[c + 1]
-        harness.harness_place(first, len(lens), Hk, x, out)
+    for x in range(len(want)):
+        split.harness_place(first, len(lens), Hk, x, out)
         assert tuple(out) == want[x]
-    # cuts moved to the boundary next to them: in order, and by no more than half a segment
-    harness.harness_snap.restype = ll
-    harness.harness_snap.argtypes = [ctypes.POINTER(i32), i32, i32, ll, ll]
-    ends = sorted({0} | {x + n - b for x, (_, _, b, n) in enumerate(want)})
-    moved = [harness.harness_snap(first, len(lens), Hk, W, b) for b in at]
-    assert moved[0] == 0 and moved[-1] == W and moved == sorted(moved) and set(moved) <= set(ends)
-    assert all(2 * abs(m - b) <= max(lens) for m, b in zip(moved, at))
 
 
-def test_work_of_the_largest_calls(harness):
+@pytest.mark.parametrize("lens,Hk", BATCHES)
+@pytest.mark.parametrize("ctas,least", [(148, 16), (7, 16), (1, 16), (296, 16)])
+def test_work_is_cut_into_parts_of_equal_cost(split, lens, Hk, ctas, least):
+    """Each block belongs to one worker, the one that kv4_worker names; every worker has one; the parts' costs differ by one."""
+    R, W = len(lens), sum(lens) * Hk
+    costs = [split.harness_cost(n) for n in lens]
+    assert all(c == (0 if n == 0 else (n + 3) // 4 * 4 + 4) for c, n in zip(costs, lens))
+    first, cost, V = prefix(lens), prefix(costs), sum(costs) * Hk
+    N = split.harness_workers(W, ctas, least)
+    assert 1 <= N <= ctas and (N == 1 or W // N >= least)
+    at = [split.harness_begin(V, N, c) for c in range(N + 1)]
+    assert at[0] == 0 and at[-1] == V and max(b - a for a, b in zip(at, at[1:])) <= V // N + 1
+    cut = [split.harness_cut(first, cost, R, Hk, v) for v in at]
+    assert cut[0] == 0 and cut[-1] == W and all(a < b for a, b in zip(cut, cut[1:]))
+    x = 0
+    for r, n in enumerate(lens):
+        for h in range(Hk):
+            for b in range(n):
+                c = split.harness_worker(cost, R, Hk, N, r, h, b)
+                assert cut[c] <= x < cut[c + 1]
+                x += 1
+    # a worker's warps: in order, from its first block to its last
+    for a, b in zip(at, at[1:]):
+        inner = [split.harness_cut(first, cost, R, Hk, a + split.harness_begin(b - a, 8, i)) for i in range(9)]
+        assert inner == sorted(inner) and inner[0] == cut[at.index(a)] and inner[-1] == cut[at.index(b)]
+
+
+@pytest.mark.parametrize("lens,Hk", BATCHES)
+@pytest.mark.parametrize("N", [1, 5, 148])
+def test_cuts_moved_to_segment_boundaries(split, lens, Hk, N):
+    """In order, by no more than half a segment, and no segment lies in two parts."""
+    R = len(lens)
+    costs = [split.harness_cost(n) for n in lens]
+    first, cost, V = prefix(lens), prefix(costs), sum(costs) * Hk
+    ends = {sum(costs[:r]) * Hk + h * c for r, c in enumerate(costs) for h in range(Hk + 1)}
+    blocks = {sum(lens[:r]) * Hk + h * n for r, n in enumerate(lens) for h in range(Hk + 1)}
+    at = [split.harness_begin(V, N, c) for c in range(N + 1)]
+    moved = [split.harness_snap(cost, R, Hk, v) for v in at]
+    assert moved[0] == 0 and moved[-1] == V and moved == sorted(moved) and set(moved) <= ends
+    assert all(2 * abs(m - v) <= max(costs) for m, v in zip(moved, at))
+    assert {split.harness_cut(first, cost, R, Hk, v) for v in moved} <= blocks
+
+
+def test_work_of_the_largest_calls(split):
     """The products of the cut stay in 64 bits at the largest tables: 2^31 blocks of 512 heads."""
-    ll, i32 = ctypes.c_longlong, ctypes.c_int
-    harness.harness_begin.restype = ll
-    harness.harness_begin.argtypes = [ll, i32, i32]
-    harness.harness_worker.argtypes = [ll, i32, ll]
-    W, N = (2 ** 31 - 1) * 512, 148 * 4
+    n, Hk, N = 2 ** 31 - 1 - 64, 512, 148 * 4
+    first, cost = prefix([n]), prefix([split.harness_cost(n)])
+    V = cost[1] * Hk
+    assert split.harness_cut(first, cost, 1, Hk, V) == n * Hk
     for c in (0, 1, 300, N - 1):
-        b = harness.harness_begin(W, N, c)
-        assert b == c * W // N and harness.harness_worker(W, N, b) == c
-        assert c == 0 or harness.harness_worker(W, N, b - 1) == c - 1
+        v = split.harness_begin(V, N, c)
+        assert v == c * V // N
+        x = split.harness_cut(first, cost, 1, Hk, v)
+        h, blk = divmod(x, n)
+        assert split.harness_worker(cost, 1, Hk, N, 0, h, blk) == c
 
 
 def test_rope_table_is_exact_far_out():
