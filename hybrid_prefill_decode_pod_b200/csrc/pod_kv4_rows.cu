@@ -36,16 +36,17 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 // costs two multiply-adds for each channel. The partner, rot / 2 channels away,
 // comes by shuffle as it was read.
 //
-// 16384 rows of 72 heads of 128: 105 us, 5.8 TB/s, 90 % of the copy rate, at four
-// CTAs an SM (64 registers); three CTAs took 115, batches of 3 or 6 at four 115
-// and 118, of 2 at five 108.
+// 16384 rows of 72 heads of 128: 104 us, 5.9 TB/s, 91 % of the copy rate, with 32
+// warps an SM (64 registers); 24 took 115, batches of 3 or 6 with 32 115 and 118,
+// of 2 with 40 108, CTAs of 256 threads 105.
 constexpr int kBatch = 4;
+constexpr int kRopeThreads = 128;
 
 template <int D, bool FP16, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const QkParams P, int parts) {
+__global__ void __launch_bounds__(kRopeThreads, 8) norm_rope_kernel(const QkParams P, int parts) {
   constexpr int kLanes = D / 8, kHeads = 32 / kLanes;
   const int lane = threadIdx.x & 31, l = lane % kLanes, sub = lane / kLanes;
-  const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int unit = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
   const int row = unit / parts, part = unit % parts;
   if (row >= P.num_rows) return;
   const int pos = __ldg(P.positions + row);
@@ -391,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_write_kernel(const Kv4Rows P)
 }
 
 // The reverse: the record comes to shared memory in 16-byte pieces, the rows
-// leave in 16 bytes a lane. 11264 tokens of 8 heads of 128: 17 us for 86 MB (13 at
+// leave in 16 bytes a lane. 11264 tokens of 8 heads of 128: 16 us for 86 MB (13 at
 // the copy rate), 1.7 waves of CTAs again.
 template <int D, int GROUP, bool FP16>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Rows P) {
@@ -416,7 +417,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Rows P) {
     __syncwarp();
     uint16_t* kd = P.x[0] + (row + sub) * P.row[0] + h * P.head[0] + 8 * l;
     uint16_t* vd = P.x[1] + (row + sub) * P.row[1] + h * P.head[1] + 8 * l;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = 0; i + sub < count; i += kRows) {
       const int t = token + i + sub;
       uint32_t kc = 0, vc = 0, kp = 0x7fff7fffu, vp = kp;  // NaN without a place
@@ -439,15 +440,16 @@ cudaError_t norm_rope_of(const QkParams& P, int interleaved, cudaStream_t s) {
   // Few rows are cut into parts of one batch of heads at least.
   constexpr int kHeads = 256 / D;
   const int most = std::max(P.heads[0], P.heads[1]);
-  const long long want = 148 * 4 * kWarps;
+  const long long want = 148 * 32;
   long long parts = std::min<long long>((want + P.num_rows - 1) / P.num_rows,
                                         (most + kHeads - 1) / kHeads);
   parts = std::max<long long>(parts, 1);
-  const unsigned grid = (unsigned)((P.num_rows * parts + kWarps - 1) / kWarps);
+  constexpr int kUnits = kRopeThreads / 32;
+  const unsigned grid = (unsigned)((P.num_rows * parts + kUnits - 1) / kUnits);
   if (interleaved)
-    norm_rope_kernel<D, FP16, true><<<grid, kThreads, 0, s>>>(P, (int)parts);
+    norm_rope_kernel<D, FP16, true><<<grid, kRopeThreads, 0, s>>>(P, (int)parts);
   else
-    norm_rope_kernel<D, FP16, false><<<grid, kThreads, 0, s>>>(P, (int)parts);
+    norm_rope_kernel<D, FP16, false><<<grid, kRopeThreads, 0, s>>>(P, (int)parts);
   return cudaGetLastError();
 }
 
