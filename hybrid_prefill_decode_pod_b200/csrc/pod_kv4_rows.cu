@@ -325,61 +325,67 @@ __device__ __forceinline__ uint4 values(uint32_t code, uint32_t sm) {
                     float_to_row2<FP16>(a.y, b.y), float_to_row2<FP16>(c.y, d.y));
 }
 
+__device__ __forceinline__ void sts32(uint32_t at, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t at, uint32_t v) {
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"((unsigned short)v) : "memory");
+}
+
 // Bound by the rows' bytes, D bytes of codes for 4 D of K and V. A whole page is
 // put together in shared memory, since V's codes of a token lie 16 bytes apart,
 // and leaves in 16-byte pieces; part of a page goes to its places directly.
 //
-// 16384 tokens of 8 heads of 128: 30 us for 85 MB (13 at the copy rate): 300 warp
-// instructions for four rows of K or V each, two thirds of the issue slots, in
-// 1.7 waves of CTAs. Two steps in flight at four CTAs an SM; three steps, or
-// five or six CTAs with fewer registers, took 1 to 10 % more.
+// 16384 tokens of 8 heads of 128: 26 us for 85 MB (13 at the copy rate): 250 warp
+// instructions for two rows of K and of V each, two thirds of the issue slots, in
+// 1.7 waves of CTAs. Four CTAs an SM (64 registers); five took 3 % more. With
+// the whole page's places computed anew for each row, through generic addresses,
+// it took 30.
 template <int D, int GROUP, bool FP16>
 __global__ void __launch_bounds__(kThreads, 4) kv4_write_kernel(const Kv4Rows P) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, NG = D / GROUP;
   constexpr int kRec = kv4_record_bytes(D, GROUP);
-  constexpr int kFlight = 2;  // steps whose rows of K and V are in flight
   __shared__ __align__(16) unsigned char stage[kWarps][kRec];
   const int lane = threadIdx.x & 31, l = lane % kLanes, sub = lane / kLanes;
   unsigned char* mine = stage[threadIdx.x >> 5];
   for_pages(P, [&](int row, int count, int token, int page, int h) {
     if (page < 0) return;
     unsigned char* rec = P.pool + ((long long)page * P.Hk + h) * kRec;
-    const bool whole = count == 16;
-    unsigned char* to = whole ? mine : rec;
     const uint16_t* ks = P.x[0] + (row + sub) * P.row[0] + h * P.head[0] + 8 * l;
     const uint16_t* vs = P.x[1] + (row + sub) * P.row[1] + h * P.head[1] + 8 * l;
-    uint4 kr[kFlight], vr[kFlight];
-    const auto load = [&](int k, int i) {
+    const auto load = [&](uint4& k, uint4& v, int i) {
       if (i + sub < count) {
-        kr[k] = *reinterpret_cast<const uint4*>(ks + i * P.row[0]);
-        vr[k] = *reinterpret_cast<const uint4*>(vs + i * P.row[1]);
+        k = *reinterpret_cast<const uint4*>(ks + i * P.row[0]);
+        v = *reinterpret_cast<const uint4*>(vs + i * P.row[1]);
       }
     };
-#pragma unroll
-    for (int k = 0; k < kFlight; ++k) {
-      kr[k] = vr[k] = make_uint4(0, 0, 0, 0);
-      load(k, k * kRows);
-    }
+    uint4 k0 = make_uint4(0, 0, 0, 0), v0 = k0, k1 = k0, v1 = k0;  // two steps in flight
+    load(k0, v0, 0);
+    load(k1, v1, kRows);
+    if (count == 16) {
+      // where token `sub` goes; i tokens on (i a multiple of kRows) the places
+      // differ by constants
+      const uint32_t at = smem_u32(mine), k_at = at + k_code_byte<D>(sub, l),
+                     v_at = at + v_code_byte<D>(sub, 2 * l),
+                     p_at = at + pair_byte<D>(0, sub, 8 * l / GROUP, NG);
+      const auto step = [&](int i, const uint4& kr, const uint4& vr) {
+        const Quantised kq = quantise<GROUP, FP16>(kr), vq = quantise<GROUP, FP16>(vr);
+        const uint32_t v_to = v_at + (32 * (i >> 3) + ((i & 7) >> 1)) * (D / 8);
+        sts32(k_at + i * (D / 2), kq.code);
+        sts16(v_to, vq.code);
+        sts16(v_to + D / 2, vq.code >> 16);
+        if (8 * l % GROUP == 0) {
+          sts32(p_at + i * NG * 4, *reinterpret_cast<const uint32_t*>(&kq.pair));
+          sts32(p_at + (kKv4Page + i) * NG * 4, *reinterpret_cast<const uint32_t*>(&vq.pair));
+        }
+      };
 #pragma unroll 1
-    for (int i = 0; i < count; i += kRows) {
-      const Quantised kq = quantise<GROUP, FP16>(kr[0]), vq = quantise<GROUP, FP16>(vr[0]);
-#pragma unroll
-      for (int k = 0; k + 1 < kFlight; ++k) {
-        kr[k] = kr[k + 1];
-        vr[k] = vr[k + 1];
+      for (int i = 0; i < 16; i += 2 * kRows) {
+        step(i, k0, v0);
+        load(k0, v0, i + 2 * kRows);
+        step(i + kRows, k1, v1);
+        load(k1, v1, i + 3 * kRows);
       }
-      load(kFlight - 1, i + kFlight * kRows);
-      if (i + sub >= count) continue;
-      const int t = token + i + sub;
-      *reinterpret_cast<uint32_t*>(to + k_code_byte<D>(t, l)) = kq.code;
-      *reinterpret_cast<uint16_t*>(to + v_code_byte<D>(t, 2 * l)) = (uint16_t)vq.code;
-      *reinterpret_cast<uint16_t*>(to + v_code_byte<D>(t, 2 * l + 1)) = (uint16_t)(vq.code >> 16);
-      if (8 * l % GROUP == 0) {
-        *reinterpret_cast<__half2*>(to + pair_byte<D>(0, t, 8 * l / GROUP, NG)) = kq.pair;
-        *reinterpret_cast<__half2*>(to + pair_byte<D>(1, t, 8 * l / GROUP, NG)) = vq.pair;
-      }
-    }
-    if (whole) {
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < (kRec + 511) / 512; ++i)
@@ -387,6 +393,23 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_write_kernel(const Kv4Rows P)
           *reinterpret_cast<uint4*>(rec + i * 512 + lane * 16) =
               *reinterpret_cast<const uint4*>(mine + i * 512 + lane * 16);
       __syncwarp();
+      return;
+    }
+#pragma unroll 1
+    for (int i = 0; i < count; i += kRows) {
+      const Quantised kq = quantise<GROUP, FP16>(k0), vq = quantise<GROUP, FP16>(v0);
+      k0 = k1;
+      v0 = v1;
+      load(k1, v1, i + 2 * kRows);
+      if (i + sub >= count) continue;
+      const int t = token + i + sub;
+      *reinterpret_cast<uint32_t*>(rec + k_code_byte<D>(t, l)) = kq.code;
+      *reinterpret_cast<uint16_t*>(rec + v_code_byte<D>(t, 2 * l)) = (uint16_t)vq.code;
+      *reinterpret_cast<uint16_t*>(rec + v_code_byte<D>(t, 2 * l + 1)) = (uint16_t)(vq.code >> 16);
+      if (8 * l % GROUP == 0) {
+        *reinterpret_cast<__half2*>(rec + pair_byte<D>(0, t, 8 * l / GROUP, NG)) = kq.pair;
+        *reinterpret_cast<__half2*>(rec + pair_byte<D>(1, t, 8 * l / GROUP, NG)) = vq.pair;
+      }
     }
   });
 }
