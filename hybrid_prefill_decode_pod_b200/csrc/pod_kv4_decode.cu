@@ -42,6 +42,7 @@
 // instructions bound it: about 225 a block at two an SM and cycle, the integer
 // pipe (the ANDs) 44 % busy, the matrix pipe 28 %.
 #include <algorithm>
+#include <cfloat>
 
 #include "pod_kv4.cuh"
 #include "pod_kv4_split.h"
@@ -68,7 +69,7 @@ constexpr int kLeast = 16;  // blocks that make another CTA worth its join
 // blocks. 16 x 1000 tokens, 8 KV heads: 16.2 us cut anywhere, 12.3 whole; 8 x 100:
 // 13.7 and 9.4.
 constexpr int kWhole = 64;
-constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.4426950408889634f;
 
 // d = a b + c: 16 x 16 times 16 x 8
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -364,7 +365,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
     const long long orow = (long long)seg.r * P.H + (long long)seg.h * G;
 
     // The queries as the second operand: column `row` is a head, chunk c's
-    // channels 32 c + 8 j + i in the order in which K's codes come apart.
+    // channels 32 c + 8 j + i in the order in which K's codes come apart. A score
+    // is p 2^24 F ln 2. (2^24 F may pass fp32 where the queries pass 2^116; cut, it
+    // still makes every weight but the largest 0.)
     uint32_t qf[NC][4];
     float qs[NP][2], F[2];
     {
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
       most = max2<FP16>(most, most >> 16);
       const int e = __float_as_int(row2_to_float<FP16>(most).x) >> 23;  // 255 for NaN too
       const float sc = e == 0 || e == 255 ? 1.f : __int_as_float(min(263 - e, 254) << 23);
-      const float f = P.scale_log2 * 16777216.f / sc;
+      const float f = P.scale_log2 / sc;
       float sum[NP];
 #pragma unroll
       for (int u = 0; u < NP; ++u) sum[u] = 0.f;
@@ -424,8 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
 
     // State of heads head0 (x) and head0 + 1 (y): O of channels 4 row + 0..3 of the
     // own groups' chunks, this lane's part of the sums of p and of p (m + 8 s).
-    float2 O[NC / REP][4], pm[NP];
-    float l[2] = {0.f, 0.f}, top[2] = {-INFINITY, -INFINITY};
+    float2 O[NC / REP][4], pm[NP], l = make_float2(0.f, 0.f);
+    float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int c = 0; c < NC / REP; ++c)
 #pragma unroll
@@ -557,27 +560,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
       }
       // ---- running maximum and sum; p becomes 2^k times the weight
       const float lift = (float)((__float_as_int(up) >> 23) - 127);
-      float2 alpha;
+      float2 alpha, base, scale;  // base: minus the maxima
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float mx = top[i];
 #pragma unroll
         for (int b = 0; b < kTile; ++b) mx = max3(mx, p[b][i], p[b][i + 2]);
         mx = rows_max(mx);
-        const float base = mx == -INFINITY ? 0.f : mx;
-        const float a = ex2((top[i] - base) * F[i]);
+        const float f = fminf(F[i] * 0x1p24f, FLT_MAX), m = mx == -INFINITY ? 0.f : -mx;
+        (i ? alpha.y : alpha.x) = ex2((top[i] + m) * f);
+        (i ? base.y : base.x) = m;
+        (i ? scale.y : scale.x) = f;
         top[i] = mx;
-        const float off = fmaf(-base, F[i], lift);
-        float s = 0.f;
-#pragma unroll
-        for (int b = 0; b < kTile; ++b) {
-          p[b][i] = ex2(fmaf(p[b][i], F[i], off));
-          p[b][i + 2] = ex2(fmaf(p[b][i + 2], F[i], off));
-          s += p[b][i] + p[b][i + 2];
-        }
-        l[i] = fmaf(l[i], a, s * down);
-        (i ? alpha.y : alpha.x) = a;
       }
+      // The maximum is taken away before the scale, so the largest weight is 2^k exactly,
+      // whatever the size of the scores.
+      float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int b = 0; b < kTile; ++b)
+#pragma unroll
+        for (int y = 0; y < 4; y += 2) {
+          const float2 x = fma2(add2(make_float2(p[b][y], p[b][y + 1]), base), scale,
+                                make_float2(lift, lift));
+          p[b][y] = ex2(x.x);
+          p[b][y + 1] = ex2(x.y);
+          s = add2(s, make_float2(p[b][y], p[b][y + 1]));
+        }
+      l = fma2(l, alpha, mul2(s, make_float2(down, down)));
       // ---- O: where a maximum moved, what is there is scaled first
       if (__any_sync(0xffffffffu, alpha.x != 1.f || alpha.y != 1.f)) {
 #pragma unroll
@@ -669,8 +678,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
     }
 
     // ---- the piece is done
-    l[0] = rows_sum(l[0]);
-    l[1] = rows_sum(l[1]);
+    l.x = rows_sum(l.x);
+    l.y = rows_sum(l.y);
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
       pm[u].x = rows_sum(pm[u].x);
@@ -691,16 +700,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
         const int page = __ldg(P.table + (long long)seg.r * P.table_stride + seg.blk + i);
         here |= page < 0 || page >= P.pool_blocks;
       }
-      if (__any_sync(0xffffffffu, here)) l[0] = l[1] = __int_as_float(0x7fffffff);
+      if (__any_sync(0xffffffffu, here)) l.x = l.y = __int_as_float(0x7fffffff);
     }
-    if (__any_sync(0xffffffffu, failed)) l[0] = l[1] = __int_as_float(0x7fffffff);
+    if (__any_sync(0xffffffffu, failed)) l.x = l.y = __int_as_float(0x7fffffff);
+    const auto score = [&](int i) { return top[i] * 0x1p24f * (F[i] * kLn2); };  // the largest
     const bool starts = seg.blk == 0, ends = seg.blk + n == seg.nblk;
     if (starts && ends) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int g = head0 + i;
         if (g >= G) continue;
-        const float inv = 1.f / l[i];
+        const float sum = i ? l.y : l.x, inv = 1.f / sum;
 #pragma unroll
         for (int c = 0; c < NC / REP; ++c) {
           const auto at = [&](int k) { return (i ? O[c][k].y : O[c][k].x) * inv; };
@@ -709,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
           v.y = float_to_row2<FP16>(at(2), at(3));
           *reinterpret_cast<uint2*>(P.o + (orow + g) * D + channel(c)) = v;
         }
-        if (row == 0 && rep == 0) P.lse[orow + g] = fmaf(top[i], F[i] * kLn2, logf(l[i]));
+        if (row == 0 && rep == 0) P.lse[orow + g] = score(i) + logf(sum);
       }
     } else {
       // the warp's last piece lies over its ring, one before others in the workspace
@@ -727,8 +737,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
                 : make_float4(O[c][0].x, O[c][1].x, O[c][2].x, O[c][3].x);
         if (row == 0 && rep == 0) {
           float* m2 = ml + ((w * 2 + at) * kMaxG + g) * 2;
-          m2[0] = top[i] * F[i];
-          m2[1] = l[i];
+          m2[0] = score(i);
+          m2[1] = i ? l.y : l.x;
         }
       }
       if (lane == 0) {
@@ -788,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
       for (uint32_t m = members; m; m &= m - 1) {
         const int y = __ffs(m) - 1, y_at = y == from ? from_at : 0;
         const float* m2 = ml + ((y * 2 + y_at) * kMaxG + g) * 2;
-        const float e = ex2(m2[0] - base);
+        const float e = ex2((m2[0] - base) * kLog2e);
         const float4 v = reinterpret_cast<const float4*>(piece_of(y, y_at))[i];
         sum = fmaf(m2[1], e, sum);
         acc.x = fmaf(v.x, e, acc.x);
@@ -803,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
         v.x = float_to_row2<FP16>(acc.x * inv, acc.y * inv);
         v.y = float_to_row2<FP16>(acc.z * inv, acc.w * inv);
         *reinterpret_cast<uint2*>(P.o + orow * D + i % (D / 4) * 4) = v;
-        if (i % (D / 4) == 0) P.lse[orow] = mx * kLn2 + logf(sum);
+        if (i % (D / 4) == 0) P.lse[orow] = mx + logf(sum);
       } else {
         reinterpret_cast<float4*>(gp)[i] = acc;
         if (i % (D / 4) == 0)
@@ -848,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
         const float2 m2 = __ldcg(reinterpret_cast<const float2*>(part + G * D + 2 * g));
         const float4 v = __ldcg(reinterpret_cast<const float4*>(part) + i);
         const float top = fmaxf(mx, m2.x), base = top == -INFINITY ? 0.f : top;
-        const float e0 = ex2(mx - base), e = ex2(m2.x - base);
+        const float e0 = ex2((mx - base) * kLog2e), e = ex2((m2.x - base) * kLog2e);
         mx = top;
         sum = fmaf(m2.y, e, sum * e0);
         acc.x = fmaf(v.x, e, acc.x * e0);
@@ -862,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
       v.x = float_to_row2<FP16>(acc.x * inv, acc.y * inv);
       v.y = float_to_row2<FP16>(acc.z * inv, acc.w * inv);
       *reinterpret_cast<uint2*>(P.o + orow * D + i % (D / 4) * 4) = v;
-      if (i % (D / 4) == 0) P.lse[orow] = mx * kLn2 + logf(sum);
+      if (i % (D / 4) == 0) P.lse[orow] = mx + logf(sum);
     }
   }
 }

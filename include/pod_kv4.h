@@ -162,7 +162,7 @@ POD_API int pod_kv4_read(pod_kv4_ctx* ctx, const pod_kv4_rows_args* args, void* 
 /* O[r, h] = softmax(q K^T / sqrt(d)) V over the tokens 0 .. ctx_lens[r] - 1
  * as the cache holds them, LSE as in pod_attn.h. Lengths are cut to
  * 0 .. 16 block_table_stride. An empty context gives O = 0 and
- * LSE = -infinity. A request with a page id outside the pool gets O = LSE =
+ * LSE = -infinity. Scores may be as large as fp32 holds. A request with a page id outside the pool gets O = LSE =
  * NaN, and so do the rows of a device-side wait that ran out (after about a
  * second). What the cache holds behind a length is never used, whatever its bits.
  * The context's workspace serves one call at a time: calls on one context,

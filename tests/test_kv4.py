@@ -616,3 +616,33 @@ def test_context_errors():
     assert kv.close() == pa.POD_OK
     with pytest.raises(ValueError):
         run_decode(kv, q[:2], pool, tab[:2], lens[:2])
+
+
+@pytest.mark.parametrize("dtype,factor", [(BF, 1e8), (BF, 1e12), (BF, 1e30), (BF, 2.0 ** 117), (HF, 8e3)])
+def test_decode_scores_of_any_size(dtype, factor):
+    """Scores far beyond 2^24 leave one token per row. Every tile of 64 tokens has values of another
+    scale, and the long context lies in several CTAs."""
+    d, group, H, Hk = 128, 64, 4, 2
+    lens = [300, 1500, 40, 1]
+    q, pool, table = decode_case(lens, H, Hk, d, group, dtype, 30)
+    q = (q.double() * factor).to(dtype)
+    par = pool[..., 16 * d:].contiguous().view(torch.float16).unflatten(-1, (2, -1))
+    if dtype == HF:
+        par[:, :, 0] *= 100
+    for r, n in enumerate(lens):
+        for blk in range(-(-n // 16)):
+            page = int(table[r, blk])
+            par[page, :, 1] = (par[page, :, 1].float() * 2.0 ** (3 * (blk // 4 % 5) - 8)).half().nan_to_num(0, 0, 0)
+    pool[..., 16 * d:] = par.flatten(-2).contiguous().view(torch.uint8)
+    # no score is near the largest: what the kernel's scores may be off is 2^-17 sum |q_i k_i| / sqrt(d)
+    for r, n in enumerate(lens):
+        if n == 1:
+            continue
+        k = ref.values(pool[table[r, :-(-n // 16)].long()], d, group).permute(2, 1, 0, 3, 4).flatten(2, 3)[0, :, :n]
+        for h in range(H):
+            kk, x = k[h // (H // Hk)], q[r, h].double()
+            two = (kk @ x / math.sqrt(d)).topk(2).values
+            assert two[0] - two[1] > max(1000, 3 * 2.0 ** -17 * (kk.abs() @ x.abs()).max() / math.sqrt(d))
+    kv = p4.PodKv4(H, Hk, d, group_size=group, dtype=dtype)
+    o, lse = run_decode(kv, q.cuda(), pool.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda())
+    check_decode(q, pool, table, lens, d, group, o, lse)
