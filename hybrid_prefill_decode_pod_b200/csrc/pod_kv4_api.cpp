@@ -15,7 +15,8 @@ struct pod_kv4_ctx {
   pod_kv4_config cfg{};
   int grid = 0;  // CTAs of the decode kernel
   float* part = nullptr;
-  int* counters = nullptr;
+  int* counters = nullptr;  // [grid] arrivals, then the status word
+  bool force = false;       // the next decode's waits run out (POD_FLAG_TEST_FORCE_TIMEOUT)
 };
 
 namespace {
@@ -181,6 +182,7 @@ int pod_kv4_create(pod_kv4_ctx** out, const pod_kv4_config* cfg) {
   if (rc) return rc;
   if (H / Hk > kMaxGroup || cfg->page_size != kKv4Page) return POD_EUNSUPPORTED;
   if (cfg->dtype != POD_DTYPE_BF16 && cfg->dtype != POD_DTYPE_FP16) return POD_EUNSUPPORTED;
+  if (cfg->flags & ~POD_FLAG_TEST_FORCE_TIMEOUT) return POD_EUNSUPPORTED;
   if (cfg->max_decode_reqs > kKv4MaxReqs || Hk > 512) return POD_ECAPACITY;
   rc = check_device(cfg->device);
   if (rc) return rc;
@@ -196,6 +198,7 @@ int pod_kv4_create(pod_kv4_ctx** out, const pod_kv4_config* cfg) {
   pod_kv4_ctx* c = new (std::nothrow) pod_kv4_ctx();
   if (!c) return POD_ENOMEM;
   c->cfg = *cfg;
+  c->force = cfg->flags & POD_FLAG_TEST_FORCE_TIMEOUT;
   int per_sm = 0;
   size_t floats = 0;
   if (kv4_decode_init(cfg->head_dim, cfg->group_size, cfg->dtype, H / Hk, cfg->max_decode_reqs,
@@ -207,8 +210,8 @@ int pod_kv4_create(pod_kv4_ctx** out, const pod_kv4_config* cfg) {
   }
   c->grid = sms * per_sm;
   if (cudaMalloc(&c->part, sizeof(float) * (floats * c->grid + 1)) != cudaSuccess ||
-      cudaMalloc(&c->counters, sizeof(int) * c->grid) != cudaSuccess ||
-      cudaMemset(c->counters, 0, sizeof(int) * c->grid) != cudaSuccess ||
+      cudaMalloc(&c->counters, sizeof(int) * (c->grid + 1)) != cudaSuccess ||
+      cudaMemset(c->counters, 0, sizeof(int) * (c->grid + 1)) != cudaSuccess ||
       cudaDeviceSynchronize() != cudaSuccess) {
     cudaGetLastError();
     pod_kv4_destroy(c);
@@ -253,6 +256,9 @@ int pod_kv4_decode(pod_kv4_ctx* c, const pod_kv4_decode_args* a, void* stream) {
   P.part = c->part;
   P.counters = c->counters;
   P.grid = c->grid;
+  P.status = c->counters + c->grid;
+  P.force = c->force;
+  c->force = false;
   DeviceGuard guard(c->cfg.device);
   if (!guard.ok) return POD_ECUDA;
   return launch_kv4_decode(P, c->cfg.head_dim, c->cfg.group_size, c->cfg.dtype,
@@ -261,12 +267,27 @@ int pod_kv4_decode(pod_kv4_ctx* c, const pod_kv4_decode_args* a, void* stream) {
              : POD_ECUDA;
 }
 
+int pod_kv4_status(pod_kv4_ctx* c, void* stream) {
+  if (!c) return POD_EINVAL;
+  DeviceGuard guard(c->cfg.device);
+  if (!guard.ok) return POD_ECUDA;
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return POD_ECUDA;
+  int st = 0, *word = c->counters + c->grid;
+  if (cudaMemcpy(&st, word, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess ||
+      cudaMemset(word, 0, sizeof(int)) != cudaSuccess)
+    return POD_ECUDA;
+  return st;
+}
+
 int pod_kv4_destroy(pod_kv4_ctx* c) {
   if (!c) return POD_OK;
   int st = POD_OK;
   {
     DeviceGuard guard(c->cfg.device);
-    if (cudaDeviceSynchronize() != cudaSuccess) st = POD_ECUDA;
+    if (cudaDeviceSynchronize() != cudaSuccess ||
+        (c->counters && cudaMemcpy(&st, c->counters + c->grid, sizeof(int),
+                                   cudaMemcpyDeviceToHost) != cudaSuccess))
+      st = POD_ECUDA;
     cudaFree(c->part);
     cudaFree(c->counters);
   }

@@ -114,12 +114,23 @@ __device__ __forceinline__ void own_pairs(uint32_t (&v)[NP], uint32_t at) {
     }
   }
 }
-// Waits for a phase of a ring slot; gives up after about a second (false).
-__device__ bool slow_wait(uint32_t bar, uint32_t parity) {
+// Waits for a phase of a ring slot; gives up after `budget` cycles (false).
+__device__ __noinline__ bool slow_wait(uint32_t bar, uint32_t parity, long long budget) {
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity))
-    if (clock64() - t0 > kDefaultWaitBudget) return false;
+    if (clock64() - t0 > budget) return false;
   return true;
+}
+constexpr int kStatusTimeout = -5;             // POD_ETIMEOUT
+constexpr long long kForcedWait = 2000000LL;   // cycles of the test's wait (~1 ms)
+
+// A wait of this warp ran out before its block `done`: waits for every copy that it
+// still has under way (issued blocks, each by its own slot and phase), so that none
+// lands in shared memory that is used for something else, and records the status.
+__device__ __noinline__ void give_up(uint32_t bars, int done, int issued, int slots, int* status) {
+  for (int i = done; i < issued; ++i) slow_wait(bars + i % slots * 8, i / slots & 1, kDefaultWaitBudget);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) atomicExch(status, kStatusTimeout);
 }
 // The upper bytes of both halves
 __device__ __forceinline__ uint32_t high_bytes(uint32_t v) { return __byte_perm(v, 0, 0x4341); }
@@ -161,9 +172,11 @@ struct Shape {
   static constexpr int kMlOff = kWarps * kRing;  // float [warp][2][kMaxG][2]
   static constexpr int kMetaOff = kMlOff + kWarps * 2 * kMaxG * 2 * 4;
   static constexpr int kMiscOff = kMetaOff + kWarps * (int)sizeof(PieceMeta);
-  static constexpr int kBarOff = (kMiscOff + 3 * kWarps * 4 + 2 * (int)sizeof(Shared) + 7) / 8 * 8;  // mbarrier [warp][slot]
+  // mbarrier [warp][slot], and one that nothing completes
+  static constexpr int kBarOff = (kMiscOff + 3 * kWarps * 4 + 2 * (int)sizeof(Shared) + 7) / 8 * 8;
+  static constexpr int kNeverOff = kBarOff + kWarps * kSlots * 8;
   // a record whose pairs are 0, for a tile of fewer than kTile blocks
-  static constexpr int kZeroOff = (kBarOff + kWarps * kSlots * 8 + 15) / 16 * 16;
+  static constexpr int kZeroOff = (kNeverOff + 8 + 15) / 16 * 16;
   static constexpr int kFirstOff = kZeroOff + kRec;
   static __host__ int smem(int reqs) { return kFirstOff + 2 * (reqs + 1) * 4; }
 };
@@ -223,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
       misc[2 * kWarps + w] = big;
     }
     if (tid < kWarps) meta[tid].has[0] = meta[tid].has[1] = 0;
-    if (tid < kWarps * kSlots) mbar_init(smem_u32(smem + S::kBarOff) + tid * 8, 1);
+    if (tid <= kWarps * kSlots) mbar_init(smem_u32(smem + S::kBarOff) + tid * 8, 1);
     fence_mbar_init();
     for (int i = tid; i < kRec / 4; i += kThreads)
       reinterpret_cast<uint32_t*>(smem + S::kZeroOff)[i] = 0;
@@ -348,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
   }
 
   int slot = 0, phase = 0;  // of the next block
-  bool failed = false;
+  bool failed = false;  // a wait of this warp ran out: what it has from there on is NaN
   for (long long x = xb; x < xe;) {
     if (x > xb) {  // the next head, or the next request that is not empty
       seg.blk = 0;
@@ -436,15 +449,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
 #pragma unroll
     for (int g = 0; g < NP; ++g) pm[g] = make_float2(0.f, 0.f);
 
-    for (int t0 = 0; t0 < n; t0 += kTile) {
+    for (int t0 = 0; t0 < n && !failed; t0 += kTile) {
       const int nb = min(kTile, n - t0);
       // lane b waits for the tile's block b
       {
         const int sl = slot + lane;
         const uint32_t bar = bar_s + (sl >= kSlots ? sl - kSlots : sl) * 8;
         const uint32_t parity = phase ^ (sl >= kSlots);
-        if (lane < nb && !mbar_try_wait(bar, parity) && !failed) failed = !slow_wait(bar, parity);
+        const int done = (int)(x - xb) + t0;
+        bool late = lane < nb && !mbar_try_wait(bar, parity) && !slow_wait(bar, parity, kDefaultWaitBudget);
+        // (a test's: warp w gives up at its tile w, or its last one)
+        if (P.force && (done >= kTile * w || done + nb == total))
+          late = !slow_wait(smem_u32(smem + S::kNeverOff), 0, kForcedWait);
         __syncwarp();
+        failed = __any_sync(0xffffffffu, late);
+        if (failed) {
+          give_up(bar_s, done, min(issued, total), kSlots, P.status);
+          break;
+        }
       }
       // The blocks' records. A tile of fewer than kTile blocks takes the zero
       // record instead, so that all of the tile's work is one run of
@@ -702,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
       }
       if (__any_sync(0xffffffffu, here)) l.x = l.y = __int_as_float(0x7fffffff);
     }
-    if (__any_sync(0xffffffffu, failed)) l.x = l.y = __int_as_float(0x7fffffff);
+    if (failed) l.x = l.y = __int_as_float(0x7fffffff);
     const auto score = [&](int i) { return top[i] * 0x1p24f * (F[i] * kLn2); };  // the largest
     const bool starts = seg.blk == 0, ends = seg.blk + n == seg.nblk;
     if (starts && ends) {
@@ -753,9 +775,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
     }
     x += n;
   }
-  // after a wait that ran out: the copies still in flight
-  for (int i = max(total - kSlots, 0); failed && i < total; ++i)
-    slow_wait(bar_s + i % kSlots * 8, i / kSlots & 1);
   __syncthreads();
 
   // ------------------------------------------------ join the warps' pieces

@@ -55,6 +55,8 @@ struct Kv4Decode {
   float* part;       // workspace: split partial results
   int* counters;     // workspace: arrivals, zero between calls
   int grid;          // CTAs that the workspace is made for
+  int* status;       // set where a wait runs out
+  int force;         // a test's: waits run out
 };
 
 cudaError_t launch_qk_norm_rope(const QkParams& P, int D, int dtype, int interleaved,

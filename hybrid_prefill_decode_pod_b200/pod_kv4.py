@@ -26,14 +26,15 @@ DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
 # Every symbol include/pod_kv4.h declares.
 EXPORTED = ("pod_qk_norm_rope", "pod_kv4_record_bytes", "pod_kv4_create", "pod_kv4_write",
-            "pod_kv4_read", "pod_kv4_decode", "pod_kv4_destroy")
+            "pod_kv4_read", "pod_kv4_decode", "pod_kv4_status", "pod_kv4_destroy")
 
-_i, _ll, _vp = ctypes.c_int, ctypes.c_longlong, ctypes.c_void_p
+_i, _u, _ll, _vp = ctypes.c_int, ctypes.c_uint, ctypes.c_longlong, ctypes.c_void_p
 
 
 class Kv4Config(ctypes.Structure):
     _fields_ = [("num_qo_heads", _i), ("num_kv_heads", _i), ("head_dim", _i), ("group_size", _i),
-                ("dtype", _i), ("page_size", _i), ("max_decode_reqs", _i), ("device", _i)]
+                ("dtype", _i), ("page_size", _i), ("max_decode_reqs", _i), ("device", _i),
+                ("flags", _u)]
 
 
 class Kv4RowsArgs(ctypes.Structure):
@@ -100,6 +101,7 @@ def _library() -> ctypes.CDLL:
         lib.pod_kv4_write.argtypes = [_vp, _vp, _vp]
         lib.pod_kv4_read.argtypes = [_vp, _vp, _vp]
         lib.pod_kv4_decode.argtypes = [_vp, _vp, _vp]
+        lib.pod_kv4_status.argtypes = [_vp, _vp]
         lib.pod_kv4_destroy.argtypes = [_vp]
         for name in EXPORTED:
             getattr(lib, name).restype = ctypes.c_int
@@ -142,12 +144,12 @@ class PodKv4:
 
     def __init__(self, num_qo_heads: int, num_kv_heads: int, head_dim: int, *,
                  group_size: int = 64, dtype: torch.dtype = torch.bfloat16,
-                 max_decode_reqs: int = 1024, device: int = 0):
+                 max_decode_reqs: int = 1024, device: int = 0, flags: int = 0):
         self._lib = _library()
         self._h = None
         _need(dtype in DTYPES, "dtype: bfloat16 or float16")
         self.cfg = Kv4Config(num_qo_heads, num_kv_heads, head_dim, group_size, DTYPES[dtype],
-                             PAGE_SIZE, max_decode_reqs, device)
+                             PAGE_SIZE, max_decode_reqs, device, flags)
         h = _vp()
         rc = self._lib.pod_kv4_create(ctypes.byref(h), ctypes.byref(self.cfg))
         if rc != POD_OK:
@@ -289,6 +291,10 @@ class PodKv4:
                                                   lse[:chunk_rows], k=list(kc.split(lens)),
                                                   v=list(vc.split(lens))), stream)
         return o, lse
+
+    def status(self, stream=None) -> int:
+        """``pod_kv4_status``: synchronises the stream; POD_ETIMEOUT after a wait that ran out."""
+        return int(self._lib.pod_kv4_status(self._h, _raw_stream(stream, self.device)))
 
     def _failed(self, rc: int, name: str) -> None:
         _need(self._h is not None, "the context is closed")

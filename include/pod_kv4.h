@@ -70,6 +70,11 @@ typedef struct {
   int page_size;       /* 16                                               */
   int max_decode_reqs; /* cap on decodes per call, 1 .. 4096               */
   int device;          /* CUDA device ordinal the context lives on         */
+  unsigned flags;      /* 0; POD_FLAG_TEST_FORCE_TIMEOUT (test only): in the
+                          context's first pod_kv4_decode warp w of each CTA
+                          waits at its tile w (64 tokens; its last one, if it
+                          has fewer) for what nothing completes, about 1 ms,
+                          and gives up                                     */
 } pod_kv4_config;
 
 /* Rows of K and V for some requests: the arguments of pod_kv4_write and
@@ -162,14 +167,21 @@ POD_API int pod_kv4_read(pod_kv4_ctx* ctx, const pod_kv4_rows_args* args, void* 
 /* O[r, h] = softmax(q K^T / sqrt(d)) V over the tokens 0 .. ctx_lens[r] - 1
  * as the cache holds them, LSE as in pod_attn.h. Lengths are cut to
  * 0 .. 16 block_table_stride. An empty context gives O = 0 and
- * LSE = -infinity. Scores may be as large as fp32 holds. A request with a page id outside the pool gets O = LSE =
- * NaN, and so do the rows of a device-side wait that ran out (after about a
- * second). What the cache holds behind a length is never used, whatever its bits.
+ * LSE = -infinity. Scores may be as large as fp32 holds. A request with a page
+ * id outside the pool gets O = LSE = NaN, and so do the rows of a device-side
+ * wait that ran out (after about a second), which pod_kv4_status then reports.
+ * What the cache holds behind a length is never used, whatever its bits.
  * The context's workspace serves one call at a time: calls on one context,
  * replays of captured ones included, must not overlap. */
 POD_API int pod_kv4_decode(pod_kv4_ctx* ctx, const pod_kv4_decode_args* args, void* stream);
 
-/* Synchronises the device and frees everything. NULL is a no-op. */
+/* Synchronises `stream`, then returns and clears the sticky device status
+ * (POD_OK, or POD_ETIMEOUT after a wait of pod_kv4_decode ran out), or
+ * POD_ECUDA if the synchronisation failed. */
+POD_API int pod_kv4_status(pod_kv4_ctx* ctx, void* stream);
+
+/* Synchronises the device, reads the sticky status, frees everything. Returns
+ * that status (POD_OK or POD_ETIMEOUT) or POD_ECUDA. NULL is a no-op. */
 POD_API int pod_kv4_destroy(pod_kv4_ctx* ctx);
 
 #ifdef __cplusplus

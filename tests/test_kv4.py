@@ -646,3 +646,31 @@ def test_decode_scores_of_any_size(dtype, factor):
     kv = p4.PodKv4(H, Hk, d, group_size=group, dtype=dtype)
     o, lse = run_decode(kv, q.cuda(), pool.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda())
     check_decode(q, pool, table, lens, d, group, o, lse)
+
+
+@pytest.mark.parametrize("lens,H,Hk,d,group", [
+    ([5000, 40, 700, 3000, 0, 300], 8, 2, 128, 64), ([5000, 40, 700, 3000, 0, 300], 8, 1, 64, 32),
+    ([100, 0, 33, 900, 1024] * 40, 4, 4, 128, 32), ([17], 2, 2, 128, 128),
+])
+def test_waits_that_run_out(lens, H, Hk, d, group):
+    """In the first call every warp gives up at one of its tiles: the rows of what it has from there
+    on are NaN, the others as ever, and the status says so. The next call is right."""
+    q, pool, table = decode_case(lens, H, Hk, d, group, BF, 31)
+    args = q.cuda(), pool.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    want, wlse = run_decode(p4.PodKv4(H, Hk, d, group_size=group), *args)
+    kv = p4.PodKv4(H, Hk, d, group_size=group, flags=pa.FLAG_TEST_FORCE_TIMEOUT)
+    o, lse = run_decode(kv, *args)
+    assert kv.status() == pa.POD_ETIMEOUT and kv.status() == pa.POD_OK   # cleared by the read
+    lost = lse.isnan().unflatten(1, (Hk, -1)).all(-1).repeat_interleave(H // Hk, 1)
+    assert lost.any() and torch.equal(lse.isnan(), lost) and torch.equal(o.isnan(), lost.unsqueeze(-1).expand_as(o))
+    assert not lost[torch.tensor(lens) == 0].any()
+    assert torch.equal(o[~lost], want[~lost]) and torch.equal(lse[~lost], wlse[~lost])
+    again = run_decode(kv, *args)
+    assert torch.equal(again[0], want) and torch.equal(again[1], wlse)
+    check_decode(q, pool, table, lens, d, group, want, wlse)
+    assert kv.status() == pa.POD_OK
+    run_decode(kv, *args)
+    assert kv.close() == pa.POD_OK
+    kv = p4.PodKv4(H, Hk, d, group_size=group, flags=pa.FLAG_TEST_FORCE_TIMEOUT)
+    run_decode(kv, *args)
+    assert kv.close() == pa.POD_ETIMEOUT

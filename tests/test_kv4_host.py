@@ -283,3 +283,13 @@ def test_binding_refuses_tensors_of_the_host():
     x = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         p4.norm_rope_args(x, x, torch.zeros(2, dtype=torch.int32), torch.zeros(5, 64))
+
+
+@pytest.mark.parametrize("flags,code", [(4, pa.POD_EUNSUPPORTED), (1, pa.POD_EUNSUPPORTED)])
+def test_create_refuses_flags(lib, flags, code):
+    h = ctypes.c_void_p()
+    assert lib.pod_kv4_create(ctypes.byref(h), ctypes.byref(p4.Kv4Config(32, 8, 128, 64, 0, 16, 64, 0, flags))) == code and not h.value
+
+
+def test_status_of_nothing(lib):
+    assert lib.pod_kv4_status(None, None) == pa.POD_EINVAL
