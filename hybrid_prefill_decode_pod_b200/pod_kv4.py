@@ -264,6 +264,10 @@ class PodKv4:
             raise ValueError("qkv, start: expected the chunks' rows and one for each decode")
         if n_pre and (pod.paged or self.dtype is not torch.bfloat16):
             raise ValueError("prefills: expected a contiguous-layout context and bfloat16")
+        # prefill_args hands on pointers alone: the context has to read and write what is behind them
+        if n_pre and any(getattr(pod.cfg, x) != getattr(self.cfg, x) for x in
+                         ("num_qo_heads", "num_kv_heads", "head_dim", "device")):
+            raise ValueError("pod: expected a context of this cache's heads, head_dim and device")
         if stream is None:
             stream = torch.cuda.current_stream(self.device)
         with torch.cuda.stream(stream):

@@ -293,3 +293,36 @@ def test_create_refuses_flags(lib, flags, code):
 
 def test_status_of_nothing(lib):
     assert lib.pod_kv4_status(None, None) == pa.POD_EINVAL
+
+
+def unopened(cls, cfg, **kw):
+    """A binding object without a library context: for what is refused before any call."""
+    x = object.__new__(cls)
+    x.cfg, x._h = cfg, None
+    for k, v in kw.items():
+        setattr(x, k, v)
+    return x
+
+
+def hybrid_call(pod_cfg=(), **kw):
+    """PodKv4.hybrid of two chunks and a decode on host tensors, 8 / 2 heads of 128."""
+    kv = unopened(p4.PodKv4, p4.Kv4Config(8, 2, 128, 64, 0, 16, 4, 0), dtype=torch.bfloat16, device=0, record=2304, _per_page=(2, 2304),
+                  _kv=(2, 128), _qo=(8, 128))
+    cfg = dict(num_qo_heads=8, num_kv_heads=2, head_dim=128, kv_layout=0, page_size=0, max_prefill_reqs=2, max_prefill_tokens=64, max_decode_reqs=1,
+               max_kv_tokens=128, device=0, flags=0)
+    cfg.update(pod_cfg)
+    pod = unopened(pa.PodAttention, pa.Config(*cfg.values()), paged=False)
+    chunks, n = kw.pop("chunk_lens", [5, 3]), kw.pop("decodes", 1)
+    rows = max(0, sum(chunks)) + n
+    i32 = lambda k: torch.zeros(k, dtype=torch.int32)  # noqa: E731
+    a = dict(qkv=torch.zeros(rows, 12, 128, dtype=torch.bfloat16), positions=i32(rows), cos_sin=torch.zeros(200, 128), chunk_lens=chunks,
+             prior_lens=[10, 0], cu_rows=i32(len(chunks) + n + 1), start=i32(len(chunks) + n), ctx_lens=i32(n),
+             pool=torch.zeros(20, 2, 2304, dtype=torch.uint8), block_table=torch.zeros(len(chunks) + n, 8, dtype=torch.int32))
+    a.update(kw)
+    return kv.hybrid(pod, **a)
+
+
+@pytest.mark.parametrize("cfg", [dict(num_qo_heads=16), dict(num_kv_heads=8), dict(head_dim=64), dict(device=1)])
+def test_hybrid_refuses_another_shapes_context(cfg):
+    with pytest.raises(ValueError, match="pod: expected a context of this cache's heads"):
+        hybrid_call(cfg)
