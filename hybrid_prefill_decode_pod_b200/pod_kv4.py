@@ -256,6 +256,9 @@ class PodKv4:
         attend over it; the prefills' contexts are read back for ``pod``, a context of the
         contiguous layout, which takes bf16."""
         H, Hk, d = self.cfg.num_qo_heads, self.cfg.num_kv_heads, self.cfg.head_dim
+        chunk_lens, prior_lens = [int(n) for n in chunk_lens], [int(n) for n in prior_lens]
+        if len(prior_lens) != len(chunk_lens) or min(chunk_lens + prior_lens, default=0) < 0:
+            raise ValueError("chunk_lens, prior_lens: expected as many of each, none negative")
         n_pre, rows = len(chunk_lens), qkv.shape[0]
         chunk_rows = sum(chunk_lens)
         if qkv.dim() != 3 or qkv.shape[1:] != (H + 2 * Hk, d):
@@ -290,7 +293,7 @@ class PodKv4:
                 vc = torch.empty_like(kc)
                 self.read(self.rows_args(cu[:n_pre + 1], cu[n_pre + 1:], kc, vc, pool,
                                          block_table[:n_pre]), stream)
-                pod.prefill_only(pod.prefill_args(list(chunk_lens), list(prior_lens),
+                pod.prefill_only(pod.prefill_args(chunk_lens, prior_lens,
                                                   q[:chunk_rows], o[:chunk_rows],
                                                   lse[:chunk_rows], k=list(kc.split(lens)),
                                                   v=list(vc.split(lens))), stream)

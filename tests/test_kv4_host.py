@@ -326,3 +326,11 @@ def hybrid_call(pod_cfg=(), **kw):
 def test_hybrid_refuses_another_shapes_context(cfg):
     with pytest.raises(ValueError, match="pod: expected a context of this cache's heads"):
         hybrid_call(cfg)
+
+
+@pytest.mark.parametrize("kw", [dict(prior_lens=[10]), dict(prior_lens=[10, 0, 7]), dict(prior_lens=[]), dict(prior_lens=[10, -1]),
+                                dict(chunk_lens=[9, -1])])
+def test_hybrid_refuses_lengths_that_do_not_fit(kw):
+    """A short list of prior lengths would be read behind its end."""
+    with pytest.raises(ValueError, match="chunk_lens, prior_lens"):
+        hybrid_call(**kw)
