@@ -18,7 +18,7 @@ from typing import Optional, Sequence
 
 import torch
 
-from .pod_attn import POD_OK, PodAttention, PodError, load_library
+from .pod_attn import POD_ECAPACITY, POD_OK, PodAttention, PodError, load_library
 
 PAGE_SIZE = 16
 _I32, _U8, _F32 = torch.int32, torch.uint8, torch.float32
@@ -271,6 +271,21 @@ class PodKv4:
         if n_pre and any(getattr(pod.cfg, x) != getattr(self.cfg, x) for x in
                          ("num_qo_heads", "num_kv_heads", "head_dim", "device")):
             raise ValueError("pod: expected a context of this cache's heads, head_dim and device")
+        # K is rotated in place and the cache written before decodes and prefills are called: what
+        # they would refuse is refused here, ahead of the first launch
+        lens = [p + c for p, c in zip(prior_lens, chunk_lens)]
+        n_all = start.numel()
+        if (ctx_lens.numel() > self.cfg.max_decode_reqs or rows > 1 << 30 or sum(lens) > 1 << 30
+                or n_all * (block_table.shape[-1] + 8) > 2 ** 31 - 1 or block_table.shape[-1] > 1 << 26
+                or pool.shape[0] * Hk > 2 ** 31 - 1
+                or chunk_rows and (n_pre > pod.cfg.max_prefill_reqs
+                                   or chunk_rows > pod.cfg.max_prefill_tokens
+                                   or any(c and n > pod.cfg.max_kv_tokens
+                                          for c, n in zip(chunk_lens, lens)))):
+            raise PodError(POD_ECAPACITY, "PodKv4.hybrid")
+        if pool.shape[0] == 0 or pool.data_ptr() % 16:
+            raise ValueError("pool: expected pages, 16-byte aligned")
+        _need(self._h is not None and not (chunk_rows and pod._h is None), "the context is closed")
         if stream is None:
             stream = torch.cuda.current_stream(self.device)
         with torch.cuda.stream(stream):
@@ -278,25 +293,29 @@ class PodKv4:
             o = torch.empty_like(q)
             lse = torch.empty(rows, H, dtype=torch.float32, device=qkv.device)
             k, v = qkv[:, H:H + Hk], qkv[:, H + Hk:]
-            qk_norm_rope(norm_rope_args(qkv[:, :H], k, positions, cos_sin, q_out=q,
-                                        q_weight=q_weight, k_weight=k_weight, eps=eps,
-                                        interleaved=interleaved), stream)
-            self.write(self.rows_args(cu_rows, start, k, v, pool, block_table), stream)
+            rope = norm_rope_args(qkv[:, :H], k, positions, cos_sin, q_out=q, q_weight=q_weight,
+                                  k_weight=k_weight, eps=eps, interleaved=interleaved)
+            write = self.rows_args(cu_rows, start, k, v, pool, block_table)
             if rows > chunk_rows:
-                self.decode(self.decode_args(ctx_lens, q[chunk_rows:], o[chunk_rows:],
-                                             lse[chunk_rows:], pool, block_table[n_pre:]), stream)
+                decode = self.decode_args(ctx_lens, q[chunk_rows:], o[chunk_rows:],
+                                          lse[chunk_rows:], pool, block_table[n_pre:])
             if chunk_rows:
-                lens = [p + c for p, c in zip(prior_lens, chunk_lens)]
                 cu = torch.tensor([sum(lens[:i]) for i in range(n_pre + 1)] + [0] * n_pre,
                                   dtype=torch.int32).to(qkv.device)
                 kc = torch.empty(sum(lens), Hk, d, dtype=self.dtype, device=qkv.device)
                 vc = torch.empty_like(kc)
-                self.read(self.rows_args(cu[:n_pre + 1], cu[n_pre + 1:], kc, vc, pool,
-                                         block_table[:n_pre]), stream)
-                pod.prefill_only(pod.prefill_args(chunk_lens, prior_lens,
-                                                  q[:chunk_rows], o[:chunk_rows],
-                                                  lse[:chunk_rows], k=list(kc.split(lens)),
-                                                  v=list(vc.split(lens))), stream)
+                read = self.rows_args(cu[:n_pre + 1], cu[n_pre + 1:], kc, vc, pool,
+                                      block_table[:n_pre])
+                prefill = pod.prefill_args(chunk_lens, prior_lens, q[:chunk_rows], o[:chunk_rows],
+                                           lse[:chunk_rows], k=list(kc.split(lens)),
+                                           v=list(vc.split(lens)))
+            qk_norm_rope(rope, stream)
+            self.write(write, stream)
+            if rows > chunk_rows:
+                self.decode(decode, stream)
+            if chunk_rows:
+                self.read(read, stream)
+                pod.prefill_only(prefill, stream)
         return o, lse
 
     def status(self, stream=None) -> int:

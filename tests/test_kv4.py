@@ -674,3 +674,31 @@ def test_waits_that_run_out(lens, H, Hk, d, group):
     kv = p4.PodKv4(H, Hk, d, group_size=group, flags=pa.FLAG_TEST_FORCE_TIMEOUT)
     run_decode(kv, *args)
     assert kv.close() == pa.POD_ETIMEOUT
+
+
+def test_refused_hybrid_calls_change_nothing():
+    """Whatever the reason, rows and cache are as they were, and the same call put right gives what a first call gives."""
+    H, Hk, d, g = 8, 2, 128, gen(32)
+    kv = p4.PodKv4(H, Hk, d, max_decode_reqs=1)
+    pods = [pa.PodAttention(H, Hk, d, max_prefill_reqs=2, max_prefill_tokens=tok, max_decode_reqs=1, max_kv_tokens=most)
+            for tok, most in ((64, 256), (49, 256), (64, 99))]
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
+    pool, tab = kv.new_pool(40), p4.rope_table(512, d)
+    x = torch.randn(51, H + 2 * Hk, d, generator=g).to(BF).cuda()
+    table = torch.arange(32, dtype=torch.int32).reshape(2, 16).cuda()
+    a = dict(qkv=x.clone(), positions=i32(list(range(50, 100)) + [20]), cos_sin=tab, chunk_lens=[50], prior_lens=[50], cu_rows=i32([0, 50, 51]),
+             start=i32([50, 20]), ctx_lens=i32([21]), pool=pool, block_table=table)
+    first = kv.hybrid(pods[0], **{**a, "qkv": x.clone(), "pool": kv.new_pool(40)})
+    odd = torch.zeros(pool.numel() + 8, dtype=torch.uint8, device="cuda")[8:].view(pool.shape)
+    bad = [(pods[1], {}), (pods[2], {}), (pods[0], dict(cu_rows=i32([0, 51]))), (pods[0], dict(pool=odd)), (pods[0], dict(pool=pool[:, :, :-16])),
+           (pods[0], dict(block_table=table[:1])), (pods[0], dict(cos_sin=tab[:, :24].contiguous())), (pods[0], dict(eps=-1.0)),
+           (pods[0], dict(ctx_lens=i32([21]).long())), (pods[0], dict(q_weight=torch.ones(d, device="cuda"))),
+           (pods[0], dict(chunk_lens=[49], ctx_lens=i32([20, 21]), start=i32([50, 20, 21]), cu_rows=i32([0, 49, 50, 51]),
+                          block_table=table[[0, 1, 1]]))]
+    for pod, kw in bad:
+        with pytest.raises((ValueError, pa.PodError)):
+            kv.hybrid(pod, **{**a, **kw})
+        assert torch.equal(a["qkv"], x) and not pool.any() and not odd.any(), kw.keys()
+    o, lse = kv.hybrid(pods[0], **a)
+    assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+    assert all(pod.status() == pa.POD_OK and pod.close() == pa.POD_OK for pod in pods)

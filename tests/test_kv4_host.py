@@ -334,3 +334,25 @@ def test_hybrid_refuses_lengths_that_do_not_fit(kw):
     """A short list of prior lengths would be read behind its end."""
     with pytest.raises(ValueError, match="chunk_lens, prior_lens"):
         hybrid_call(**kw)
+
+
+@pytest.mark.parametrize("pod_cfg,kw", [
+    (dict(), dict(decodes=5)),                                   # the cache's context takes 4 decodes
+    (dict(), dict(chunk_lens=[1] * 3, prior_lens=[0] * 3)), (dict(max_prefill_tokens=7), dict()), (dict(max_kv_tokens=14), dict()),
+    (dict(max_kv_tokens=2), dict(chunk_lens=[0, 1], prior_lens=[0, 2])),
+])
+def test_hybrid_refuses_sizes_before_it_changes_anything(pod_cfg, kw):
+    with pytest.raises(pa.PodError) as e:
+        hybrid_call(pod_cfg, **kw)
+    assert e.value.code == pa.POD_ECAPACITY
+
+
+@pytest.mark.parametrize("pool", [torch.zeros(0, 2, 2304, dtype=torch.uint8), torch.zeros(2 * 2304 + 8, dtype=torch.uint8)[8:].view(1, 2, 2304)])
+def test_hybrid_refuses_a_pool_that_no_call_takes(pool):
+    with pytest.raises(ValueError, match="pool"):
+        hybrid_call(pool=pool)
+
+
+def test_hybrid_of_closed_contexts():
+    with pytest.raises(ValueError, match="closed"):
+        hybrid_call()
