@@ -249,12 +249,15 @@ class PodKv4:
         :meth:`PodAttention.hybrid` from the projection's output on. Returns O and LSE.
 
         ``qkv`` [rows, H + 2 Hk, d] holds the chunks of the prefill requests and then one row
-        for each decode; its q and k heads are normed and rotated in place. ``chunk_lens`` and
-        ``prior_lens`` are host lengths as in :meth:`PodAttention.prefill_args`; ``cu_rows``,
+        for each decode; its k heads are normed and rotated in place (q's in a tensor of their
+        own). ``chunk_lens`` and ``prior_lens`` are host lengths as in :meth:`PodAttention.prefill_args`; ``cu_rows``,
         ``start`` and ``block_table`` cover all requests, the prefills first, and ``ctx_lens``
         the decodes (their new token included). The new K and V go into the cache; decodes
         attend over it; the prefills' contexts are read back for ``pod``, a context of the
-        contiguous layout, which takes bf16."""
+        contiguous layout, which takes bf16 (an fp16 cache has decodes only).
+
+        Asynchronous like the calls it makes. What can be refused is refused before anything is
+        enqueued."""
         H, Hk, d = self.cfg.num_qo_heads, self.cfg.num_kv_heads, self.cfg.head_dim
         chunk_lens, prior_lens = [int(n) for n in chunk_lens], [int(n) for n in prior_lens]
         if len(prior_lens) != len(chunk_lens) or min(chunk_lens + prior_lens, default=0) < 0:
@@ -300,8 +303,10 @@ class PodKv4:
                 decode = self.decode_args(ctx_lens, q[chunk_rows:], o[chunk_rows:],
                                           lse[chunk_rows:], pool, block_table[n_pre:])
             if chunk_rows:
+                # (from pinned memory: the call does not wait for the stream)
                 cu = torch.tensor([sum(lens[:i]) for i in range(n_pre + 1)] + [0] * n_pre,
-                                  dtype=torch.int32).to(qkv.device)
+                                  dtype=torch.int32, pin_memory=True)
+                cu = cu.to(qkv.device, non_blocking=True)
                 kc = torch.empty(sum(lens), Hk, d, dtype=self.dtype, device=qkv.device)
                 vc = torch.empty_like(kc)
                 read = self.rows_args(cu[:n_pre + 1], cu[n_pre + 1:], kc, vc, pool,

@@ -702,3 +702,41 @@ def test_refused_hybrid_calls_change_nothing():
     o, lse = kv.hybrid(pods[0], **a)
     assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
     assert all(pod.status() == pa.POD_OK and pod.close() == pa.POD_OK for pod in pods)
+
+
+def hybrid_case(kv, g, chunks=(50, 13), prior=(20, 0), seen=(0, 3, 40)):
+    """Arguments of a hybrid call over a cache that holds something for every request (tables of 16 pages, 512 positions)."""
+    H, Hk, d = kv.cfg.num_qo_heads, kv.cfg.num_kv_heads, kv.cfg.head_dim
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
+    n, rows = len(chunks) + len(seen), sum(chunks) + len(seen)
+    at = [sum(chunks[:i]) for i in range(len(chunks) + 1)]
+    return dict(qkv=torch.randn(rows, H + 2 * Hk, d, generator=g).to(kv.dtype).cuda(), cos_sin=p4.rope_table(512, d),
+                positions=i32([p for c, s in zip(chunks, prior) for p in range(s, s + c)] + list(seen)), chunk_lens=list(chunks), prior_lens=list(prior),
+                cu_rows=i32(at + [at[-1] + 1 + i for i in range(len(seen))]), start=i32(list(prior) + list(seen)), ctx_lens=i32([s + 1 for s in seen]),
+                pool=random_pool(16 * n, Hk, d, kv.cfg.group_size, g).cuda(),
+                block_table=torch.randperm(16 * n, generator=g).reshape(n, 16).to(torch.int32).cuda())
+
+
+def test_hybrid_on_a_stream_of_its_own_does_not_wait():
+    """The call returns while the stream is still busy with what came before, and gives what it gives elsewhere."""
+    kv = p4.PodKv4(8, 2, 128)
+    pods = [pa.PodAttention(8, 2, 128, max_prefill_reqs=2, max_prefill_tokens=64, max_decode_reqs=1, max_kv_tokens=256) for _ in range(2)]
+    a = hybrid_case(kv, gen(33))
+    copies = [{**a, "qkv": a["qkv"].clone(), "pool": a["pool"].clone()} for _ in range(2)]
+    want = kv.hybrid(pods[0], **copies[0])
+    assert pods[0].status() == pa.POD_OK
+    side = torch.cuda.Stream()
+    kv.hybrid(pods[1], **{**a, "qkv": a["qkv"].clone(), "pool": a["pool"].clone()}, stream=side)   # (buffers of that stream exist)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)                                  # about 0.2 s
+        busy = torch.cuda.Event()
+        busy.record()
+    got = kv.hybrid(pods[1], **copies[1], stream=side)
+    assert not busy.query()
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert torch.equal(copies[0]["qkv"], copies[1]["qkv"]) and torch.equal(copies[0]["pool"], copies[1]["pool"])
+    assert not torch.equal(copies[0]["qkv"][:, 8:10], a["qkv"][:, 8:10])                  # k, rotated in place
+    assert torch.equal(copies[0]["qkv"][:, :8], a["qkv"][:, :8]) and torch.equal(copies[0]["qkv"][:, 10:], a["qkv"][:, 10:])
+    assert all(pod.status() == pa.POD_OK and pod.close() == pa.POD_OK for pod in pods)
