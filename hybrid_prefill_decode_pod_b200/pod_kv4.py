@@ -6,8 +6,9 @@ cache of 4-bit codes (:meth:`PodKv4.write`), reading rows back
 (:meth:`PodKv4.decode`), and the step before all of them, the per-head norm of
 q and k with the position rotation (:func:`qk_norm_rope`).
 
-Lengths, positions and tables are device tensors, so every call can be captured
-into a CUDA graph and replayed with what its tensors hold then. As in
+Their lengths, positions and tables are device tensors, so each can be captured
+into a CUDA graph and replayed with what its tensors hold then (of
+:meth:`PodKv4.hybrid`, calls without prefills can). As in
 :mod:`.pod_attn` there is no fallback: a missing library raises.
 """
 from __future__ import annotations
@@ -18,7 +19,7 @@ from typing import Optional, Sequence
 
 import torch
 
-from .pod_attn import POD_ECAPACITY, POD_OK, PodAttention, PodError, load_library
+from .pod_attn import POD_ECAPACITY, POD_EUNSUPPORTED, POD_OK, PodAttention, PodError, load_library
 
 PAGE_SIZE = 16
 _I32, _U8, _F32 = torch.int32, torch.uint8, torch.float32
@@ -257,7 +258,8 @@ class PodKv4:
         contiguous layout, which takes bf16 (an fp16 cache has decodes only).
 
         Asynchronous like the calls it makes. What can be refused is refused before anything is
-        enqueued."""
+        enqueued. A call without prefills can be captured; one with prefills, whose plan is made
+        on the host, raises POD_EUNSUPPORTED then."""
         H, Hk, d = self.cfg.num_qo_heads, self.cfg.num_kv_heads, self.cfg.head_dim
         chunk_lens, prior_lens = [int(n) for n in chunk_lens], [int(n) for n in prior_lens]
         if len(prior_lens) != len(chunk_lens) or min(chunk_lens + prior_lens, default=0) < 0:
@@ -292,6 +294,8 @@ class PodKv4:
         if stream is None:
             stream = torch.cuda.current_stream(self.device)
         with torch.cuda.stream(stream):
+            if chunk_rows and torch.cuda.is_current_stream_capturing():
+                raise PodError(POD_EUNSUPPORTED, "PodKv4.hybrid of prefills in a captured stream")
             q = torch.empty(rows, H, d, dtype=self.dtype, device=qkv.device)
             o = torch.empty_like(q)
             lse = torch.empty(rows, H, dtype=torch.float32, device=qkv.device)

@@ -740,3 +740,31 @@ def test_hybrid_on_a_stream_of_its_own_does_not_wait():
     assert not torch.equal(copies[0]["qkv"][:, 8:10], a["qkv"][:, 8:10])                  # k, rotated in place
     assert torch.equal(copies[0]["qkv"][:, :8], a["qkv"][:, :8]) and torch.equal(copies[0]["qkv"][:, 10:], a["qkv"][:, 10:])
     assert all(pod.status() == pa.POD_OK and pod.close() == pa.POD_OK for pod in pods)
+
+
+def test_hybrid_in_a_graph():
+    """Decodes are captured and replayed; prefills are refused before anything is enqueued."""
+    kv = p4.PodKv4(8, 2, 128, dtype=HF)
+    a = hybrid_case(kv, gen(34), chunks=(), prior=())
+    pool = a["pool"].clone()
+    want = kv.hybrid(None, **{**a, "qkv": a["qkv"].clone(), "pool": pool})
+    qkv = torch.empty_like(a["qkv"])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = kv.hybrid(None, **{**a, "qkv": qkv})
+    for _ in range(2):
+        qkv.copy_(a["qkv"])
+        g.replay()
+        assert all(torch.equal(x, y) for x, y in zip(out, want)) and torch.equal(a["pool"], pool)
+    kv = p4.PodKv4(8, 2, 128)
+    pod = pa.PodAttention(8, 2, 128, max_prefill_reqs=2, max_prefill_tokens=64, max_decode_reqs=1, max_kv_tokens=256)
+    a = hybrid_case(kv, gen(35))
+    before = a["qkv"].clone(), a["pool"].clone()
+    g2 = torch.cuda.CUDAGraph()
+    with pytest.raises(pa.PodError) as e:
+        with torch.cuda.graph(g2):
+            kv.hybrid(pod, **a)
+    assert e.value.code == pa.POD_EUNSUPPORTED
+    assert torch.equal(a["qkv"], before[0]) and torch.equal(a["pool"], before[1])
+    kv.hybrid(pod, **a)
+    assert pod.status() == pa.POD_OK and pod.close() == pa.POD_OK
