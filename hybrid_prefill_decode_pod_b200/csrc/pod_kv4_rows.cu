@@ -284,6 +284,9 @@ __device__ __forceinline__ Quantised quantise(const uint4& raw) {
   const uint32_t nan = 0x7fff7fffu;
   q.pair = fine ? __halves2half2(__float2half_rn(step), __float2half_rn(lo))
                 : *reinterpret_cast<const __half2*>(&nan);
+  // m + 15 s may round to infinity in fp16 (0 .. 65504: s = 4368): s one step lower does not
+  if (FP16 && fmaf(15.f, __low2float(q.pair), __high2float(q.pair)) >= 65520.f)
+    *reinterpret_cast<uint32_t*>(&q.pair) -= 1;
   const float s = __low2float(q.pair), m = __high2float(q.pair);
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));

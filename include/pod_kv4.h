@@ -18,7 +18,8 @@
  *     n = min(max(rint((x - m) / s), 0), 15)     (n = 0 where s = 0)
  *
  * with lo, hi the group's least and largest value, the difference, its
- * fifteenth and the quotient rounded to fp32. Values beyond +-65504 are
+ * fifteenth and the quotient rounded to fp32. (In fp16 rows s is one fp16 step
+ * lower where m + 15 s would round to infinity, at 65520 and above.) Values beyond +-65504 are
  * cut to it. A group that holds an infinity or a NaN gets s = m = NaN: it
  * reads back as NaN throughout, and attention over it gives NaN. Where hi - lo
  * is below about 1e-3 the spacing of small fp16 numbers (2^-24) adds up to

@@ -768,3 +768,45 @@ def test_hybrid_in_a_graph():
     assert torch.equal(a["qkv"], before[0]) and torch.equal(a["pool"], before[1])
     kv.hybrid(pod, **a)
     assert pod.status() == pa.POD_OK and pod.close() == pa.POD_OK
+
+
+def test_finite_fp16_rows_stay_finite():
+    """Groups that end near 65504, where n s + m would pass fp16: written, read back and attended over."""
+    d, group = 64, 32
+    x = torch.rand(16, 1, d, generator=gen(36)).to(HF)
+    ends = [(0, 65504), (-65504, 65504), (60000, 65504), (65472, 65504), (-65504, -65504), (65504, 65504), (-100, 65000), (1, 65504)]
+    for t in range(16):
+        for half in range(2):
+            lo, hi = ends[(t + half) % len(ends)]
+            row = x[t, 0, half * group:(half + 1) * group]
+            row.copy_((lo + (hi - lo) * row.double()).to(HF))
+            row[3], row[17] = lo, hi
+    assert x.isfinite().all()
+    kv = p4.PodKv4(1, 1, d, group_size=group, dtype=HF)
+    pool, xc = kv.new_pool(1), x.cuda()
+    cu, start, tab = (torch.tensor(v, dtype=torch.int32).cuda() for v in ([0, 16], [0], [[0]]))
+    kv.write(kv.rows_args(cu, start, xc, xc, pool, tab))
+    k, v = torch.zeros_like(xc), torch.zeros_like(xc)
+    kv.read(kv.rows_args(cu, start, k, v, pool, tab))
+    n, s, m, _ = ref.quantised(x, group)
+    gn, gs, gm = (y[0, 0] for y in ref.unpack(pool.cpu(), d, group))
+    # the pairs: as the formula has them, or one step of fp16 lower where they would pass 65520
+    over = 15 * s + m >= 65520
+    lower = (s.half().view(torch.int16) - over.to(torch.int16)).view(HF).double()
+    assert over.any() and not over.all()
+    for i in range(2):
+        assert torch.equal(gs[i], lower[:, 0]) and torch.equal(gm[i], m[:, 0])
+    for y in (k, v):
+        assert y.isfinite().all()
+        # half a step, the 15 / 2048 of a step by which s may be rounded or one step lower by, and the output's rounding (32 below 65504)
+        assert ((y.cpu().double() - x.double()).abs() <= (0.5 + 15 * 2.0 ** -10) * s + 16).all()
+    q = torch.zeros(1, 1, d, dtype=HF).cuda()
+    o, lse = run_decode(kv, q, pool, tab, torch.tensor([16], dtype=torch.int32).cuda())
+    check_decode(q, pool, tab, [16], d, group, o, lse)
+    # one token alone: its values, the largest among them
+    for t in (0, 1, 5):
+        one = kv.new_pool(1)
+        kv.write(kv.rows_args(torch.tensor([0, 1], dtype=torch.int32).cuda(), start, xc[t:t + 1], xc[t:t + 1], one, tab))
+        o, lse = run_decode(kv, q, one, tab, torch.tensor([1], dtype=torch.int32).cuda())
+        assert o.isfinite().all()
+        check_decode(q, one, tab, [1], d, group, o, lse)
