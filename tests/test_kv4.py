@@ -810,3 +810,28 @@ def test_finite_fp16_rows_stay_finite():
         o, lse = run_decode(kv, q, one, tab, torch.tensor([1], dtype=torch.int32).cuda())
         assert o.isfinite().all()
         check_decode(q, one, tab, [1], d, group, o, lse)
+
+
+def test_write_far_pages():
+    """Records whose byte offsets pass 32 bits: new rows leave there what they leave in a small pool, whole pages and parts of pages."""
+    d, group, Hk, lens, starts = 128, 64, 4, [200, 50, 3], [0, 7, 30]
+    kv = p4.PodKv4(Hk, Hk, d, group_size=group)
+    table, cu, start = rows_case(lens, starts, 24, 37)
+    small = kv.new_pool(24)
+    blocks = (1 << 33) // (Hk * kv.record)
+    pool = torch.empty(blocks, Hk, kv.record, dtype=torch.uint8, device="cuda")
+    far = blocks - 24
+    pool[far:] = 0
+    # where offsets of the low 32 bits would lead
+    low = [(((far + i) * Hk * kv.record) & 0xffffffff) // (Hk * kv.record) for i in (0, 23)]
+    pool[low[0]:low[1] + 2] = 0
+    x = torch.randn(sum(lens), 2 * Hk, d, generator=gen(38)).to(BF).cuda()
+    tc = (table + far * (table >= 0)).int().cuda()
+    kv.write(kv.rows_args(cu.cuda(), start.cuda(), x[:, :Hk], x[:, Hk:], small, table.cuda()))
+    kv.write(kv.rows_args(cu.cuda(), start.cuda(), x[:, :Hk], x[:, Hk:], pool, tc))
+    assert torch.equal(pool[far:], small) and small.any()
+    assert not pool[low[0]:low[1] + 2].any()
+    k, v = torch.zeros(sum(lens), Hk, d, dtype=BF, device="cuda"), torch.zeros(sum(lens), Hk, d, dtype=BF, device="cuda")
+    kv.read(kv.rows_args(cu.cuda(), start.cuda(), k, v, pool, tc))
+    # half a step of a group whose range is below 10, and roundings
+    assert (k.float() - x[:, :Hk].float()).abs().max() < 0.5 and (v.float() - x[:, Hk:].float()).abs().max() < 0.5
