@@ -835,3 +835,29 @@ def test_write_far_pages():
     kv.read(kv.rows_args(cu.cuda(), start.cuda(), k, v, pool, tc))
     # half a step of a group whose range is below 10, and roundings
     assert (k.float() - x[:, :Hk].float()).abs().max() < 0.5 and (v.float() - x[:, Hk:].float()).abs().max() < 0.5
+
+
+def rag(n, least, most, seed):
+    g = gen(seed)
+    return torch.randint(least, most + 1, (n,), generator=g).tolist()
+
+
+@pytest.mark.parametrize("lens,H,Hk,d,group,dtype", [
+    (rag(20, 300, 3000, 40), 8, 2, 128, 64, BF),      # 148 workers, segments over two or three CTAs
+    ([0, 1100, 0] + rag(8, 1, 3000, 41) + [0], 16, 4, 128, 32, HF),
+    (rag(30, 1000, 2500, 42), 8, 1, 64, 64, BF),
+    ([12000] * 4, 2, 2, 64, 32, HF), ([2600] * 30, 7, 1, 128, 128, BF),
+])
+def test_decode_that_fills_the_grid(lens, H, Hk, d, group, dtype):
+    """All CTAs at work on contexts that go over their ends: heads and tails joined between CTAs, and calls that follow on
+    each other find the counters as they should."""
+    assert sum(-(-n // 16) for n in lens) * Hk >= 16 * 148 and max(lens) > 1024
+    assert len(lens) * Hk * int(math.sqrt(0.6 * -(-max(lens) // 16))) >= 148
+    q, pool, table = decode_case(lens, H, Hk, d, group, dtype, 43)
+    kv = p4.PodKv4(H, Hk, d, group_size=group, dtype=dtype)
+    args = q.cuda(), pool.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    outs = [run_decode(kv, *args) for _ in range(4)]
+    check_decode(q, pool, table, lens, d, group, *outs[0])
+    for o, lse in outs[1:]:
+        assert torch.equal(o, outs[0][0]) and torch.equal(lse, outs[0][1])
+    assert kv.status() == pa.POD_OK
