@@ -81,12 +81,13 @@ _pack_qk = _packer(QkArgs).pack
 
 
 class Args:
-    """The C struct of one call, and the tensors it points into."""
+    """The C struct of one call, what that call is (its kind, and the shapes that the struct
+    does not hold), and the tensors it points into."""
 
-    __slots__ = ("struct", "device", "keep")
+    __slots__ = ("struct", "call", "device", "keep")
 
-    def __init__(self, packed: bytes, device: int, keep: tuple):
-        self.struct, self.device, self.keep = packed, device, keep
+    def __init__(self, packed: bytes, call: tuple, device: int, keep: tuple):
+        self.struct, self.call, self.device, self.keep = packed, call, device, keep
 
 
 _bound = None
@@ -162,6 +163,8 @@ class PodKv4:
         self._per_page = (int(num_kv_heads), self.record)
         self._kv = (int(num_kv_heads), int(head_dim))
         self._qo = (int(num_qo_heads), int(head_dim))
+        self._rows_call = ("rows", self._kv, self.record, dtype, self.device)
+        self._decode_call = ("decode", self._qo, self._kv, self.record, dtype, self.device)
 
     def new_pool(self, pool_blocks: int) -> torch.Tensor:
         """A zeroed pool (every code and pair stands for 0)."""
@@ -201,7 +204,7 @@ class PodKv4:
         return Args(_pack_rows(n, shape[0], cu_rows.data_ptr(), start.data_ptr(), k.data_ptr(),
                                v.data_ptr(), ks[0], ks[1], vs[0], vs[1], pool.data_ptr(), blocks,
                                block_table.data_ptr(), pages),
-                    dev, (cu_rows, start, k, v, pool, block_table))
+                    self._rows_call, dev, (cu_rows, start, k, v, pool, block_table))
 
     def decode_args(self, ctx_lens, q, o, lse, pool, block_table) -> Args:
         dev, dtype = self.device, self.dtype
@@ -224,20 +227,26 @@ class PodKv4:
         return Args(_pack_decode(n, ctx_lens.data_ptr(), q.data_ptr(), o.data_ptr(),
                                  lse.data_ptr(), pool.data_ptr(), blocks, block_table.data_ptr(),
                                  pages),
-                    dev, (ctx_lens, q, o, lse, pool, block_table))
+                    self._decode_call, dev, (ctx_lens, q, o, lse, pool, block_table))
 
     # -- calls
     def write(self, args: Args, stream=None) -> None:
+        if args.call != self._rows_call:
+            raise ValueError("write: expected rows_args of this cache's shape")
         rc = self._lib.pod_kv4_write(self._h, args.struct, _raw_stream(stream, self.device))
         if rc != POD_OK:
             self._failed(rc, "pod_kv4_write")
 
     def read(self, args: Args, stream=None) -> None:
+        if args.call != self._rows_call:
+            raise ValueError("read: expected rows_args of this cache's shape")
         rc = self._lib.pod_kv4_read(self._h, args.struct, _raw_stream(stream, self.device))
         if rc != POD_OK:
             self._failed(rc, "pod_kv4_read")
 
     def decode(self, args: Args, stream=None) -> None:
+        if args.call != self._decode_call:
+            raise ValueError("decode: expected decode_args of this cache's shape")
         rc = self._lib.pod_kv4_decode(self._h, args.struct, _raw_stream(stream, self.device))
         if rc != POD_OK:
             self._failed(rc, "pod_kv4_decode")
@@ -362,6 +371,7 @@ def rope_table(max_position: int, rot_dim: int, base: float = 10000.0, *,
 
 
 _NOTHING = (0, 0, 0, 0, 0, 0, 0)  # a side that is left out
+_ROPE_CALL = ("norm_rope",)
 
 
 def _side(name, x, out, weight, rows, d, dtype, device):
@@ -417,11 +427,13 @@ def norm_rope_args(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positio
     return Args(_pack_qk(qs[0], ks[0], d, rot, 1 if interleaved else 0, DTYPES[dtype], device, rows,
                          qs[1], ks[1], qs[2], ks[2], qs[3], qs[4], ks[3], ks[4], qs[5], qs[6],
                          ks[5], ks[6], qw, kw, eps, positions.data_ptr(), cos_sin.data_ptr(), far),
-                device, (q, k, positions, cos_sin, q_out, k_out, q_weight, k_weight))
+                _ROPE_CALL, device, (q, k, positions, cos_sin, q_out, k_out, q_weight, k_weight))
 
 
 def qk_norm_rope(args: Args, stream=None) -> None:
     """``pod_qk_norm_rope``: per-head RMS norm of q and k and the rotation, in one launch."""
+    if args.call != _ROPE_CALL:
+        raise ValueError("qk_norm_rope: expected norm_rope_args")
     rc = _library().pod_qk_norm_rope(args.struct, _raw_stream(stream, args.device))
     if rc != POD_OK:
         raise PodError(rc, "pod_qk_norm_rope")

@@ -861,3 +861,20 @@ def test_decode_that_fills_the_grid(lens, H, Hk, d, group, dtype):
     for o, lse in outs[1:]:
         assert torch.equal(o, outs[0][0]) and torch.equal(lse, outs[0][1])
     assert kv.status() == pa.POD_OK
+
+
+def test_arguments_go_to_contexts_of_their_shape():
+    """Two contexts of one shape take each other's; one of other heads or groups refuses them."""
+    lens = [40, 7]
+    q, pool, table = decode_case(lens, 4, 2, 64, 64, BF, 44)
+    qc, pc, tc, lc = q.cuda(), pool.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    a, b = (p4.PodKv4(4, 2, 64, group_size=64, max_decode_reqs=n) for n in (2, 9))
+    o, lse = torch.empty_like(qc), torch.empty(2, 4, device="cuda")
+    args = a.decode_args(lc, qc, o, lse, pc, tc)
+    b.decode(args)
+    check_decode(q, pool, table, lens, 64, 64, o, lse)
+    for other in (p4.PodKv4(2, 2, 64), p4.PodKv4(4, 2, 64, group_size=32), p4.PodKv4(4, 2, 64, dtype=HF)):
+        with pytest.raises(ValueError):
+            other.decode(args)
+    with pytest.raises(ValueError):
+        a.write(args)

@@ -356,3 +356,16 @@ def test_hybrid_refuses_a_pool_that_no_call_takes(pool):
 def test_hybrid_of_closed_contexts():
     with pytest.raises(ValueError, match="closed"):
         hybrid_call()
+
+
+def test_arguments_of_another_call_are_refused():
+    """Their structs would be read as something else: other kinds, other heads, records, types and devices."""
+    calls = {"rows": ("rows", (2, 128), 2304, torch.bfloat16, 0), "decode": ("decode", (8, 128), (2, 128), 2304, torch.bfloat16, 0)}
+    kv = unopened(p4.PodKv4, p4.Kv4Config(8, 2, 128, 64, 0, 16, 4, 0), _rows_call=calls["rows"], _decode_call=calls["decode"])
+    others = [("rows", (4, 128), 2304, torch.bfloat16, 0), ("rows", (2, 128), 2560, torch.bfloat16, 0), ("rows", (2, 128), 2304, torch.float16, 0),
+              ("rows", (2, 128), 2304, torch.bfloat16, 1), ("decode", (16, 128), (2, 128), 2304, torch.bfloat16, 0), p4._ROPE_CALL]
+    for name, f, own in (("write", kv.write, "rows"), ("read", kv.read, "rows"), ("decode", kv.decode, "decode"), ("qk_norm_rope", p4.qk_norm_rope, None)):
+        for call in others + list(calls.values()):
+            if call != calls.get(own) and not (own is None and call == p4._ROPE_CALL):
+                with pytest.raises(ValueError, match=name + ": expected"):
+                    f(p4.Args(b"", call, 0, ()))
