@@ -16,7 +16,7 @@ struct pod_kv4_ctx {
   int grid = 0;  // CTAs of the decode kernel
   float* part = nullptr;
   int* counters = nullptr;  // [grid] arrivals, then the status word
-  bool force = false;       // the next decode's waits run out (POD_FLAG_TEST_FORCE_TIMEOUT)
+  bool force = false;       // the next decode leaves copies out (POD_FLAG_TEST_FORCE_TIMEOUT)
 };
 
 namespace {

@@ -14,33 +14,40 @@
 //    the rows of the product and the G <= 8 heads its columns, so no row is
 //    padding. Each channel group is summed by itself in fp32 and
 //    score = s (sum q n) + m (sum q) joins them.
-//  * V^T p as well: rows are channels, columns heads, the same subnormals times
-//    the weights p s, rounded to fp16. What the rounding costs is the weight's
-//    error times n - 8, not n: eight of each rounded weight are taken away and
-//    sum p (m + 8 s) in fp32 puts them back unrounded. So that the weights lie
-//    high in fp16, each 64 tokens scale them by a power of two that brings the
-//    largest s to [2^13, 2^14): a weight is then off by 2^-11 of itself, or by
-//    2^-39 of the largest possible one where it is below 2^-28 of that (together
-//    below 2^-19 of a million tokens' weight). With bf16 weights (2^-8) the error
+//  * V^T p as well: rows are channels, columns heads, the same subnormals
+//    times the weights p s, rounded to fp16. What the rounding costs is the
+//    weight's error times n - 8, not n: eight of each rounded weight are
+//    taken away and sum p (m + 8 s) in fp32 puts them back unrounded. (Half
+//    of the rows take whole bytes n0 + 16 n1, from which 16 n1 is taken away
+//    after the sums: those are of up to 256 s and lose four of fp32's bits,
+//    2^-16 of 16 s in all.) So that the weights lie high in fp16, each 64
+//    tokens scale them by a power of two that brings the largest s to [2^13,
+//    2^14): a weight is then off by 2^-11 of itself, or by 2^-39 of the
+//    largest possible one where it is below 2^-28 of that (together below
+//    2^-19 of a million tokens' weight). With bf16 weights (2^-8) the error
 //    of an fp16 output was several times that of its own rounding.
 //  * The running maximum and sum, scores, weights and O are fp32; one rescale
 //    every 64 tokens.
 //
 // Work: see pod_kv4_split.h. The line of blocks is cut into parts of equal cost
-// over the CTAs and each of those over its warps, so lengths need no balance and
-// no plan from the host. (Cut into equal numbers of blocks, 256 contexts of 1 to
-// 1000 tokens took 83 us, in order of length 160; by cost 46 and 47.) Warps stream their blocks, one bulk copy each, through
-// rings of their own, across segments. What a warp has of a segment that it does
-// not hold whole is joined first in its CTA, then, where the segment leaves the
-// CTA, through the workspace by the CTA that arrives last, in the order of the
-// tokens: the result does not depend on the order of arrival.
+// over the CTAs and each of those over its warps, so lengths need no balance
+// and no plan from the host. (Cut into equal numbers of blocks, 256 contexts of
+// 1 to 1000 tokens took 83 us, in order of length 160; by cost 46 and 47.)
+// Warps stream their blocks, one bulk copy each, through rings of their own,
+// across segments. What a warp has of a segment that it does not hold whole is
+// joined first in its CTA, then, where the segment leaves the CTA, through the
+// workspace by the CTA that arrives last, in the order of the tokens: the
+// result does not depend on the order of arrival.
 //
-// Measured on a B200 (L2 not warm): 64 x 4096 tokens of 8 KV heads, G = 4, groups
-// of 64: 72 us, 4.2 TB/s; 16 x 16K..32K, G = 8: 113 us, 4.2 TB/s; 128 x 0.5K..8K,
-// G = 4, groups of 32: 156 us, 4.5 TB/s. The copies alone, with the joins, take
-// 59, 85 and 120 us; with the records in L2 the last but one takes 101, so the
-// instructions bound it: about 225 a block at two an SM and cycle, the integer
-// pipe (the ANDs) 44 % busy, the matrix pipe 28 %.
+// Measured on B200s (a call, L2 not warm; they differ by 5 %): 64 x 4096 tokens
+// of 8 KV heads, G = 4, groups of 64: 71 to 72 us, 4.2 TB/s; 16 x 16K..32K, G =
+// 8: 108 to 113 us, 4.3 TB/s; 128 x 0.5K..8K, G = 4, groups of 32: 146 to 155
+// us, 4.7 TB/s. The copies alone, with the joins, took 59, 85 and 120 us where
+// all took 72, 113 and 156, the second 101 with its records in L2. 240 to 260
+// warp instructions a block fill 44 to 49 % of the issue slots, the integer
+// pipe (the ANDs) is 44 % busy, the matrix pipe 25 to 28 %: what bounds it is
+// latency, two warps a scheduler that go through a tile's products, maximum,
+// weights and products one after the other.
 #include <algorithm>
 #include <cfloat>
 
@@ -52,9 +59,10 @@
 namespace pod {
 namespace {
 
-// 8 warps of up to 255 registers: 12 of 168 issue more at a time, but spill and
-// begin more pieces (113 against 118 us for the long case, 72 against 75 for 64 x
-// 4096), 16 of 128 took 133 and 77.
+// 8 warps of up to 255 registers (36 to 40 bytes spilled at D = 128, groups of 32,
+// G > 4; none elsewhere): 12 of 168 issue more at a time, but spill and begin more
+// pieces (113 against 118 us for the long case, 72 against 75 for 64 x 4096, before
+// the last steps), 16 of 128 took 133 and 77.
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 // Blocks of 16 tokens between two rescales: 2 took 127 us for the long case, 4
@@ -63,6 +71,7 @@ constexpr int kTile = 4;
 constexpr int kSlots = 8;  // blocks in a warp's ring; 10 change nothing, 5 cost 1 %
 constexpr int kKeys = 4;   // blocks whose scores are taken together
 constexpr int kMaxG = 8;
+constexpr int kNever = -2;
 constexpr int kLeast = 16;  // blocks that make another CTA worth its join
 // Up to this many blocks in the longest context (1024 tokens) a segment stays in
 // one CTA: the joins between CTAs take about 4 us, in which a CTA does some 64
@@ -121,16 +130,20 @@ __device__ __noinline__ bool slow_wait(uint32_t bar, uint32_t parity, long long 
     if (clock64() - t0 > budget) return false;
   return true;
 }
-constexpr int kStatusTimeout = -5;             // POD_ETIMEOUT
-constexpr long long kForcedWait = 2000000LL;   // cycles of the test's wait (~1 ms)
+constexpr int kStatusTimeout = -5;  // POD_ETIMEOUT
+// (about 1 ms where a test makes waits run out)
+__device__ __forceinline__ long long budget(const Kv4Decode& P) {
+  return P.force ? kDefaultWaitBudget / 1000 : kDefaultWaitBudget;
+}
 
 // A wait of this warp ran out before its block `done`: waits for every copy that it
 // still has under way (issued blocks, each by its own slot and phase), so that none
 // lands in shared memory that is used for something else, and records the status.
-__device__ __noinline__ void give_up(uint32_t bars, int done, int issued, int slots, int* status) {
-  for (int i = done; i < issued; ++i) slow_wait(bars + i % slots * 8, i / slots & 1, kDefaultWaitBudget);
+__device__ __noinline__ void give_up(uint32_t bars, int done, int issued, int slots,
+                                     const Kv4Decode& P) {
+  for (int i = done; i < issued; ++i) slow_wait(bars + i % slots * 8, i / slots & 1, budget(P));
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) atomicExch(status, kStatusTimeout);
+  if ((threadIdx.x & 31) == 0) atomicExch(P.status, kStatusTimeout);
 }
 // The upper bytes of both halves
 __device__ __forceinline__ uint32_t high_bytes(uint32_t v) { return __byte_perm(v, 0, 0x4341); }
@@ -172,11 +185,10 @@ struct Shape {
   static constexpr int kMlOff = kWarps * kRing;  // float [warp][2][kMaxG][2]
   static constexpr int kMetaOff = kMlOff + kWarps * 2 * kMaxG * 2 * 4;
   static constexpr int kMiscOff = kMetaOff + kWarps * (int)sizeof(PieceMeta);
-  // mbarrier [warp][slot], and one that nothing completes
+  // mbarrier [warp][slot]
   static constexpr int kBarOff = (kMiscOff + 3 * kWarps * 4 + 2 * (int)sizeof(Shared) + 7) / 8 * 8;
-  static constexpr int kNeverOff = kBarOff + kWarps * kSlots * 8;
   // a record whose pairs are 0, for a tile of fewer than kTile blocks
-  static constexpr int kZeroOff = (kNeverOff + 8 + 15) / 16 * 16;
+  static constexpr int kZeroOff = (kBarOff + kWarps * kSlots * 8 + 15) / 16 * 16;
   static constexpr int kFirstOff = kZeroOff + kRec;
   static __host__ int smem(int reqs) { return kFirstOff + 2 * (reqs + 1) * 4; }
 };
@@ -236,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
       misc[2 * kWarps + w] = big;
     }
     if (tid < kWarps) meta[tid].has[0] = meta[tid].has[1] = 0;
-    if (tid <= kWarps * kSlots) mbar_init(smem_u32(smem + S::kBarOff) + tid * 8, 1);
+    if (tid < kWarps * kSlots) mbar_init(smem_u32(smem + S::kBarOff) + tid * 8, 1);
     fence_mbar_init();
     for (int i = tid; i < kRec / 4; i += kThreads)
       reinterpret_cast<uint32_t*>(smem + S::kZeroOff)[i] = 0;
@@ -305,7 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
                  zero_s = smem_u32(smem + S::kZeroOff);
 
   // Lane i of `cur` has the record of block 32 b + i, of `nxt` that of the 32
-  // behind; -1 where the page id lies outside the pool.
+  // behind; -1 where the page id lies outside the pool. (kNever, in a test: this
+  // block's copy is left out.)
   Kv4Place seg{0, 0, 0, 1};  // of the first block, once every lane has it from lane 0
   const auto records = [&](int base) {
     int rec = 0;
@@ -314,6 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
       if (base == 0) seg = p;
       const int page = __ldg(P.table + (long long)p.r * P.table_stride + p.blk);
       rec = page >= 0 && page < P.pool_blocks ? page * Hk + p.h : -1;
+      if (P.force && base + lane == min(kTile * w, total - 1)) rec = kNever;
     }
     return rec;
   };
@@ -330,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
       if (rec >= 0) {
         mbar_expect_tx(bar_s + sl * 8, kRec);
         bulk_load(ring_s + sl * kRec, P.pool + (long long)rec * kRec, kRec, bar_s + sl * 8);
-      } else {
+      } else if (rec != kNever) {
         mbar_arrive(bar_s + sl * 8);
         bad = true;
       }
@@ -456,15 +470,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const Kv4Decode
         const int sl = slot + lane;
         const uint32_t bar = bar_s + (sl >= kSlots ? sl - kSlots : sl) * 8;
         const uint32_t parity = phase ^ (sl >= kSlots);
-        const int done = (int)(x - xb) + t0;
-        bool late = lane < nb && !mbar_try_wait(bar, parity) && !slow_wait(bar, parity, kDefaultWaitBudget);
-        // (a test's: warp w gives up at its tile w, or its last one)
-        if (P.force && (done >= kTile * w || done + nb == total))
-          late = !slow_wait(smem_u32(smem + S::kNeverOff), 0, kForcedWait);
+        const bool late =
+            lane < nb && !mbar_try_wait(bar, parity) && !slow_wait(bar, parity, budget(P));
         __syncwarp();
         failed = __any_sync(0xffffffffu, late);
         if (failed) {
-          give_up(bar_s, done, min(issued, total), kSlots, P.status);
+          give_up(bar_s, (int)(x - xb) + t0, min(issued, total), kSlots, P);
           break;
         }
       }

@@ -8,6 +8,7 @@ namespace pod {
 
 constexpr int kKv4Page = 16;
 constexpr int kKv4MaxReqs = 4096;
+constexpr int kKv4Sms = 148;  // of a B200: what the row kernels' grids are shaped for
 
 // Bytes of one (page, KV head) record: 4-bit codes of K and V, then a pair
 // (scale, least value) of fp16 for each token and channel group.
@@ -56,7 +57,7 @@ struct Kv4Decode {
   int* counters;     // workspace: arrivals, zero between calls
   int grid;          // CTAs that the workspace is made for
   int* status;       // set where a wait runs out
-  int force;         // a test's: waits run out
+  int force;         // a test's: one copy of each warp is left out
 };
 
 cudaError_t launch_qk_norm_rope(const QkParams& P, int D, int dtype, int interleaved,

@@ -231,21 +231,21 @@ class PodKv4:
 
     # -- calls
     def write(self, args: Args, stream=None) -> None:
-        if args.call != self._rows_call:
+        if args.call is not self._rows_call and args.call != self._rows_call:
             raise ValueError("write: expected rows_args of this cache's shape")
         rc = self._lib.pod_kv4_write(self._h, args.struct, _raw_stream(stream, self.device))
         if rc != POD_OK:
             self._failed(rc, "pod_kv4_write")
 
     def read(self, args: Args, stream=None) -> None:
-        if args.call != self._rows_call:
+        if args.call is not self._rows_call and args.call != self._rows_call:
             raise ValueError("read: expected rows_args of this cache's shape")
         rc = self._lib.pod_kv4_read(self._h, args.struct, _raw_stream(stream, self.device))
         if rc != POD_OK:
             self._failed(rc, "pod_kv4_read")
 
     def decode(self, args: Args, stream=None) -> None:
-        if args.call != self._decode_call:
+        if args.call is not self._decode_call and args.call != self._decode_call:
             raise ValueError("decode: expected decode_args of this cache's shape")
         rc = self._lib.pod_kv4_decode(self._h, args.struct, _raw_stream(stream, self.device))
         if rc != POD_OK:
@@ -432,7 +432,7 @@ def norm_rope_args(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positio
 
 def qk_norm_rope(args: Args, stream=None) -> None:
     """``pod_qk_norm_rope``: per-head RMS norm of q and k and the rotation, in one launch."""
-    if args.call != _ROPE_CALL:
+    if args.call is not _ROPE_CALL and args.call != _ROPE_CALL:
         raise ValueError("qk_norm_rope: expected norm_rope_args")
     rc = _library().pod_qk_norm_rope(args.struct, _raw_stream(stream, args.device))
     if rc != POD_OK:

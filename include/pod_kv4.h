@@ -73,9 +73,9 @@ typedef struct {
   int device;          /* CUDA device ordinal the context lives on         */
   unsigned flags;      /* 0; POD_FLAG_TEST_FORCE_TIMEOUT (test only): in the
                           context's first pod_kv4_decode warp w of each CTA
-                          waits at its tile w (64 tokens; its last one, if it
-                          has fewer) for what nothing completes, about 1 ms,
-                          and gives up                                     */
+                          leaves out the copy of its block 4 w (its last one,
+                          if it has fewer), waits for it about 1 ms and gives
+                          up                                               */
 } pod_kv4_config;
 
 /* Rows of K and V for some requests: the arguments of pod_kv4_write and
