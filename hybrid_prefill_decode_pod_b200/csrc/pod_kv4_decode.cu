@@ -43,8 +43,8 @@
 // of 8 KV heads, G = 4, groups of 64: 71 to 72 us, 4.2 TB/s; 16 x 16K..32K, G =
 // 8: 108 to 113 us, 4.3 TB/s; 128 x 0.5K..8K, G = 4, groups of 32: 146 to 155
 // us, 4.7 TB/s. The copies alone, with the joins, took 59, 85 and 120 us where
-// all took 72, 113 and 156, the second 101 with its records in L2. 240 to 260
-// warp instructions a block fill 44 to 49 % of the issue slots, the integer
+// all took 72, 113 and 156, the second 101 with its records in L2. 240 to 256
+// warp instructions a block fill 44 to 48 % of the issue slots, the integer
 // pipe (the ANDs) is 44 % busy, the matrix pipe 25 to 28 %: what bounds it is
 // latency, two warps a scheduler that go through a tile's products, maximum,
 // weights and products one after the other.
@@ -59,7 +59,7 @@
 namespace pod {
 namespace {
 
-// 8 warps of up to 255 registers (36 to 40 bytes spilled at D = 128, groups of 32,
+// 8 warps of up to 255 registers (40 bytes spilled at D = 128, groups of 32,
 // G > 4; none elsewhere): 12 of 168 issue more at a time, but spill and begin more
 // pieces (113 against 118 us for the long case, 72 against 75 for 64 x 4096, before
 // the last steps), 16 of 128 took 133 and 77.

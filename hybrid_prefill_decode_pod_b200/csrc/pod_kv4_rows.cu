@@ -36,9 +36,10 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 // costs two multiply-adds for each channel. The partner, rot / 2 channels away,
 // comes by shuffle as it was read.
 //
-// 16384 rows of 72 heads of 128: 104 us, 5.9 TB/s, 91 % of the copy rate, with 32
-// warps an SM (64 registers); 24 took 115, batches of 3 or 6 with 32 115 and 118,
-// of 2 with 40 108, CTAs of 256 threads 105.
+// 16384 rows of 72 heads of 128: 104 us, 5.9 TB/s, 91 % of the copy rate, with
+// 32 warps an SM (64 registers, 16 bytes spilled for fp16 halves); 24 took 115,
+// batches of 3 or 6 with 32 115 and 118, of 2 with 40 108, CTAs of 256 threads
+// 105.
 constexpr int kBatch = 4;
 constexpr int kRopeThreads = 128;
 
@@ -241,7 +242,9 @@ __device__ __forceinline__ void for_pages(const Kv4Rows& P, F f) {
 // time: low halves hold least values, high halves the negated largest. A NaN or
 // an infinity shows in them. Quotients often lie on the border of two codes
 // (short significands), so the product with the approximate reciprocal is
-// corrected by one residual step, which rounds it correctly. Where a value lies
+// corrected by one residual step: off by 2^-40 of itself before its rounding, it
+// is exact on a border, and elsewhere the nearest fp32 number unless the quotient
+// lies that near to the middle of two. Where a value lies
 // outside the codes (fp16(lo) may be above lo, and values are cut to fp16's
 // range) the lane takes its codes once more, with limits.
 struct Quantised {
@@ -335,15 +338,17 @@ __device__ __forceinline__ void sts16(uint32_t at, uint32_t v) {
   asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"((unsigned short)v) : "memory");
 }
 
-// Bound by the rows' bytes, D bytes of codes for 4 D of K and V. A whole page is
+// Its floor is the rows' bytes, D bytes of codes for 4 D of K and V. A whole page is
 // put together in shared memory, since V's codes of a token lie 16 bytes apart,
 // and leaves in 16-byte pieces; part of a page goes to its places directly.
 //
-// 16384 tokens of 8 heads of 128: 26 us for 85 MB (13 at the copy rate): 250 warp
-// instructions for two rows of K and of V each, two thirds of the issue slots, in
-// 1.7 waves of CTAs. Four CTAs an SM (64 registers); five took 3 % more. With
-// the whole page's places computed anew for each row, through generic addresses,
-// it took 30.
+// 16384 tokens of 8 heads of 128, kernel alone: 26 us for 85 MB (13 at the copy
+// rate). 250 warp instructions for two rows of K and of V each are some 15 us of
+// issue slots (65 % in use while CTAs run); the largest stall is the wait for
+// memory: a warp has one page, whose first rows wait for the lookup of its request
+// and page, and the CTAs make 1.7 waves. Four CTAs an SM (64 registers, 16 to 24
+// bytes spilled); five took 3 % more. With the whole page's places
+// computed anew for each row, through generic addresses, it took 30.
 template <int D, int GROUP, bool FP16>
 __global__ void __launch_bounds__(kThreads, 4) kv4_write_kernel(const Kv4Rows P) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, NG = D / GROUP;
@@ -418,8 +423,9 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_write_kernel(const Kv4Rows P)
 }
 
 // The reverse: the record comes to shared memory in 16-byte pieces, the rows
-// leave in 16 bytes a lane. 11264 tokens of 8 heads of 128: 16 us for 86 MB (13 at
-// the copy rate), 1.7 waves of CTAs again.
+// leave in 16 bytes a lane. 16366 tokens of 8 heads of 128, kernel alone: 17 us for
+// 86 MB (13 at the copy rate), 1.7 waves of CTAs again; 61 % of the issue slots in
+// use, the largest stall again the wait for memory.
 template <int D, int GROUP, bool FP16>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Rows P) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, NG = D / GROUP;
@@ -466,7 +472,7 @@ cudaError_t norm_rope_of(const QkParams& P, int interleaved, cudaStream_t s) {
   // Few rows are cut into parts of one batch of heads at least.
   constexpr int kHeads = 256 / D;
   const int most = std::max(P.heads[0], P.heads[1]);
-  const long long want = 148 * 32;
+  const long long want = kKv4Sms * 32;
   long long parts = std::min<long long>((want + P.num_rows - 1) / P.num_rows,
                                         (most + kHeads - 1) / kHeads);
   parts = std::max<long long>(parts, 1);
@@ -483,7 +489,7 @@ template <int D, int GROUP>
 cudaError_t rows_of(const Kv4Rows& P, int dtype, bool read, cudaStream_t s) {
   // With few rows every KV head has CTAs of its own.
   const unsigned windows = (unsigned)((P.num_rows + 15) / 16);
-  const dim3 grid(windows, windows >= 2 * 148 ? (P.Hk + kWarps - 1) / kWarps : P.Hk);
+  const dim3 grid(windows, windows >= 2 * kKv4Sms ? (P.Hk + kWarps - 1) / kWarps : P.Hk);
   if (read) {
     if (dtype)
       kv4_read_kernel<D, GROUP, true><<<grid, kThreads, 0, s>>>(P);
