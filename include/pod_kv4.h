@@ -137,7 +137,8 @@ typedef struct {
 
 /* y = x / sqrt(mean(x^2) + eps) * weight over the d channels of each head,
  * then each pair (a, b) of rotated channels becomes (a cos - b sin,
- * a sin + b cos), in fp32 with one rounding at the end. A row whose position
+ * a sin + b cos), in fp32 with one rounding at the end (a head whose mean
+ * square passes fp32 becomes 0). A row whose position
  * is negative is padding: neither read nor written. One at max_position or
  * beyond has no angle: its outputs are NaN.
  * Returns POD_OK, POD_EINVAL, POD_EUNSUPPORTED, POD_ECAPACITY or POD_ECUDA. */
